@@ -12,14 +12,19 @@ from .binding import (  # noqa: F401
     NbError,
     attn_bwd_workspace_size,
     attn_fwd_bwd_host_workspace_size,
+    attn_kv4_decode_workspace_size,
+    kv4_page_bytes,
     lib,
     nb_attn_bwd,
     nb_attn_bwd_causal,
     nb_attn_fwd,
     nb_attn_fwd_bwd_host,
     nb_attn_fwd_causal,
+    nb_attn_kv4_decode,
     nb_batch_ceiling,
     nb_kernel_error,
+    nb_kv4_read,
+    nb_kv4_write,
     nb_status_string,
     nb_tokenize_batch,
     nb_tokenize_kmer,

@@ -38,6 +38,11 @@ _SIGS = [
     ("nb_tokenize_kmer", _I, [_P, ctypes.c_int64, _P, _P, _I, _P]),
     ("nb_tokenize_batch", _I, [_P, _P, _I, _I, _P, _P, _I, _P]),
     ("nb_batch_ceiling", _I, [_P, _I, _I, ctypes.POINTER(ctypes.c_int32)]),
+    ("nb_kv4_page_bytes", ctypes.c_size_t, [_I]),
+    ("nb_kv4_write", _I, [_P] * 6 + [_I] * 7 + [_P]),
+    ("nb_kv4_read", _I, [_P] * 6 + [_I] * 7 + [_P]),
+    ("nb_attn_kv4_decode_workspace_size", ctypes.c_size_t, [_I] * 8),
+    ("nb_attn_kv4_decode", _I, [_P] * 7 + [ctypes.c_size_t] + [_I] * 9 + [_P]),
 ]
 
 
@@ -185,3 +190,46 @@ def nb_batch_ceiling(offsets, batch, k=6) -> int:
     st = lib().nb_batch_ceiling(off.ctypes.data if off.size else None, batch, k, ctypes.byref(out))
     _check(st, "nb_batch_ceiling")
     return int(out.value)
+
+
+def kv4_page_bytes(d) -> int:
+    """Bytes of one head's page of the 4-bit cache (0 for an unsupported d)."""
+    return int(lib().nb_kv4_page_bytes(d))
+
+
+def nb_kv4_write(k, v, cache, block_table, starts, counts, batch, kv_heads, n, d, max_pages,
+                 num_pages, dtype, stream=None, check=True):
+    st = lib().nb_kv4_write(_ptr(k), _ptr(v), _ptr(cache), _ptr(block_table), _ptr(starts),
+                            _ptr(counts), batch, kv_heads, n, d, max_pages, num_pages, dtype,
+                            _stream(stream))
+    if check:
+        _check(st, "nb_kv4_write")
+    return st
+
+
+def nb_kv4_read(cache, block_table, starts, counts, k, v, batch, kv_heads, n, d, max_pages,
+                num_pages, dtype, stream=None, check=True):
+    st = lib().nb_kv4_read(_ptr(cache), _ptr(block_table), _ptr(starts), _ptr(counts), _ptr(k),
+                           _ptr(v), batch, kv_heads, n, d, max_pages, num_pages, dtype,
+                           _stream(stream))
+    if check:
+        _check(st, "nb_kv4_read")
+    return st
+
+
+def attn_kv4_decode_workspace_size(batch, heads, kv_heads, d, max_pages, window, sinks,
+                                   dtype) -> int:
+    return int(lib().nb_attn_kv4_decode_workspace_size(batch, heads, kv_heads, d, max_pages, window,
+                                                       sinks, dtype))
+
+
+def nb_attn_kv4_decode(q, cache, block_table, lengths, o, lse, workspace, workspace_bytes, batch,
+                       heads, kv_heads, d, max_pages, num_pages, window, sinks, dtype, stream=None,
+                       check=True):
+    st = lib().nb_attn_kv4_decode(_ptr(q), _ptr(cache), _ptr(block_table), _ptr(lengths), _ptr(o),
+                                  _ptr(lse), _ptr(workspace), workspace_bytes, batch, heads,
+                                  kv_heads, d, max_pages, num_pages, window, sinks, dtype,
+                                  _stream(stream))
+    if check:
+        _check(st, "nb_attn_kv4_decode")
+    return st

@@ -54,6 +54,7 @@ nb_status check_device() {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Shape checks shared by forward and backward.
 nb_status check_shape(int batch, int heads, int n, int d, int R, int dtype) {
@@ -136,6 +137,51 @@ nb_status attn_bwd(const void* q, const void* k, const void* v, const void* o, c
                              n, d, R, causal);
   cudaError_t e = nb::launch_attn_bwd_bf16(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? NB_OK : NB_ERR_CUDA;
+}
+
+// Shape checks of the 4-bit cache calls.  Positions, rows and grid sizes fit 31 bits.
+nb_status check_kv4(int batch, int kv_heads, int d, int max_pages, int num_pages) {
+  if (batch < 0 || kv_heads < 1 || max_pages < 0 || num_pages < 0) return NB_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return NB_ERR_UNSUPPORTED;
+  if (max_pages >= INT32_MAX / NB_KV4_PAGE) return NB_ERR_UNSUPPORTED;
+  return NB_OK;
+}
+
+nb_status kv4_rows(const void* k, const void* v, const void* cache, const int32_t* table,
+                   const int32_t* starts, const int32_t* counts, int batch, int kv_heads, int n,
+                   int d, int max_pages, int num_pages, int dtype, void* stream, bool write) {
+  nb_status st = check_kv4(batch, kv_heads, d, max_pages, num_pages);
+  if (st != NB_OK) return st;
+  if (n < 0 || (dtype != NB_F32 && dtype != NB_BF16)) return NB_ERR_INVALID_ARG;
+  const double rows = static_cast<double>(batch) * kv_heads * n;
+  if (rows > INT32_MAX) return NB_ERR_UNSUPPORTED;
+  if (rows == 0) return NB_OK;
+  // a table without pages maps nothing, so it and the pool may then be null
+  if (!k || !v || (max_pages > 0 && !table) || (max_pages > 0 && num_pages > 0 && !cache))
+    return NB_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || !aligned4(table) ||
+      !aligned4(starts) || !aligned4(counts))
+    return NB_ERR_MISALIGNED;
+  st = check_device();
+  if (st != NB_OK) return st;
+  nb::Kv4Args a = {const_cast<void*>(k), const_cast<void*>(v), const_cast<void*>(cache), table,
+                   starts, counts, error_word(), batch, kv_heads, n, d, max_pages, num_pages,
+                   dtype == NB_F32};
+  const cudaError_t e = nb::launch_kv4(a, write, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? NB_OK : NB_ERR_CUDA;
+}
+
+// Shape checks of the single-token attention over the 4-bit cache.
+nb_status check_decode(int batch, int heads, int kv_heads, int d, int max_pages, int num_pages,
+                       int window, int sinks, int dtype) {
+  nb_status st = check_kv4(batch, kv_heads, d, max_pages, num_pages);
+  if (st != NB_OK) return st;
+  if (heads < 0 || heads % kv_heads != 0 || window < 1 || sinks < 0) return NB_ERR_INVALID_ARG;
+  if (dtype != NB_F32 && dtype != NB_BF16) return NB_ERR_INVALID_ARG;
+  if (dtype != NB_BF16 || sinks > NB_MAX_SINKS) return NB_ERR_UNSUPPORTED;
+  // rows of partial results, and blocks, fit 31 bits
+  if (static_cast<double>(batch) * heads * 256 > INT32_MAX) return NB_ERR_UNSUPPORTED;
+  return NB_OK;
 }
 
 }  // namespace
@@ -268,6 +314,61 @@ nb_status nb_batch_ceiling(const int64_t* offsets, int batch, int k, int32_t* n_
   if (ceil32 > INT32_MAX) return NB_ERR_INVALID_ARG;
   *n_pad = static_cast<int32_t>(ceil32);
   return NB_OK;
+}
+
+size_t nb_kv4_page_bytes(int d) {
+  return d == 64 || d == 128 ? static_cast<size_t>(nb::kv4_page_bytes(d)) : 0;
+}
+
+nb_status nb_kv4_write(const void* k, const void* v, void* cache, const int32_t* block_table,
+                       const int32_t* starts, const int32_t* counts, int batch, int kv_heads, int n,
+                       int d, int max_pages, int num_pages, int dtype, void* stream) {
+  return kv4_rows(k, v, cache, block_table, starts, counts, batch, kv_heads, n, d, max_pages,
+                  num_pages, dtype, stream, true);
+}
+
+nb_status nb_kv4_read(const void* cache, const int32_t* block_table, const int32_t* starts,
+                      const int32_t* counts, void* k, void* v, int batch, int kv_heads, int n,
+                      int d, int max_pages, int num_pages, int dtype, void* stream) {
+  return kv4_rows(k, v, cache, block_table, starts, counts, batch, kv_heads, n, d, max_pages,
+                  num_pages, dtype, stream, false);
+}
+
+size_t nb_attn_kv4_decode_workspace_size(int batch, int heads, int kv_heads, int d, int max_pages,
+                                         int window, int sinks, int dtype) {
+  if (check_decode(batch, heads, kv_heads, d, max_pages, 0, window, sinks, dtype) != NB_OK) return 0;
+  if (batch == 0 || heads == 0) return 0;
+  nb::Kv4DecodeArgs a = {};
+  a.batch = batch; a.heads = heads; a.kv_heads = kv_heads; a.d = d;
+  a.max_pages = max_pages; a.window = window; a.sinks = sinks;
+  return nb::kv4_decode_workspace_bytes(a);
+}
+
+nb_status nb_attn_kv4_decode(const void* q, const void* cache, const int32_t* block_table,
+                             const int32_t* lengths, void* o, float* lse, void* workspace,
+                             size_t workspace_bytes, int batch, int heads, int kv_heads, int d,
+                             int max_pages, int num_pages, int window, int sinks, int dtype,
+                             void* stream) {
+  nb_status st =
+      check_decode(batch, heads, kv_heads, d, max_pages, num_pages, window, sinks, dtype);
+  if (st != NB_OK) return st;
+  if (batch == 0 || heads == 0) return NB_OK;
+  if (!q || !o || (max_pages > 0 && !block_table) || (max_pages > 0 && num_pages > 0 && !cache))
+    return NB_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(cache) || !aligned4(block_table) ||
+      !aligned4(lengths) || !aligned4(lse))
+    return NB_ERR_MISALIGNED;
+  nb::Kv4DecodeArgs a = {q, cache, block_table, lengths, o, lse, workspace, nullptr, batch, heads,
+                         kv_heads, d, max_pages, num_pages, window, sinks};
+  const size_t need = nb::kv4_decode_workspace_bytes(a);
+  if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+                   workspace_bytes < need))
+    return NB_ERR_WORKSPACE;
+  st = check_device();
+  if (st != NB_OK) return st;
+  a.err = error_word();
+  const cudaError_t e = nb::launch_kv4_decode(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? NB_OK : NB_ERR_CUDA;
 }
 
 }  // extern "C"

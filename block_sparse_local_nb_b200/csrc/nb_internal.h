@@ -30,6 +30,31 @@ struct AttnArgs {
   bool causal;        // causal band: key blocks i - R..i of query block i, keys k <= q
 };
 
+// Arguments of a write to or a read from the 4-bit cache.
+struct Kv4Args {
+  void* k;  // write: input; read: output
+  void* v;
+  void* cache;
+  const int32_t* table;
+  const int32_t* starts;  // may be null = 0
+  const int32_t* counts;  // may be null = n
+  int* err;
+  int batch, kv_heads, n, d, max_pages, num_pages;
+  bool f32;
+};
+
+struct Kv4DecodeArgs {
+  const void* q;
+  const void* cache;
+  const int32_t* table;
+  const int32_t* lengths;
+  void* o;
+  float* lse;
+  void* workspace;
+  int* err;
+  int batch, heads, kv_heads, d, max_pages, num_pages, window, sinks;
+};
+
 size_t bwd_workspace_bytes(int64_t rows, int d);
 __host__ __device__ inline int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
@@ -103,5 +128,9 @@ cudaError_t launch_tokenize_batch(const uint8_t* seqs, const int64_t* offsets, i
 cudaError_t launch_attn_fwd_f32(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_fwd_bf16_tc(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_bwd_bf16(const AttnArgs& a, cudaStream_t stream);
+int kv4_page_bytes(int d);  // d = 64 or 128
+cudaError_t launch_kv4(const Kv4Args& a, bool write, cudaStream_t stream);
+size_t kv4_decode_workspace_bytes(const Kv4DecodeArgs& a);
+cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t stream);
 
 }  // namespace nb

@@ -1,6 +1,7 @@
 /*
- * nb.h - C ABI of the B200 (sm_100a) banded block-sparse local attention and
- * the fused 2-bit DNA k-mer tokenizer.
+ * nb.h - C ABI of the B200 (sm_100a) banded block-sparse local attention, the
+ * fused 2-bit DNA k-mer tokenizer, and the operators that serve a causal model
+ * over long sequences: a 4-bit key/value cache and single-token attention over it.
  *
  * The operations follow the NucleoByte page ("NucleoByte: GPU-Accelerated
  * Block-Sparse Genomic Language Model"):
@@ -35,8 +36,8 @@
  *     returns NB_ERR_CUDA.  Kernels never trap.
  *   - Attention tensors are [batch, heads, n, d] contiguous with d innermost;
  *     log-sum-exp and the row term are [batch, heads, n] fp32.  n must be a
- *     multiple of 32 and d is 64 or 128.  Tensor pointers must be 16-byte
- *     aligned.
+ *     multiple of 32 (any n for nb_kv4_*) and d is 64 or 128.
+ *     Tensor pointers must be 16-byte aligned.
  *   - `lengths` (optional, int32 [batch], device) gives each sequence's true
  *     length L_b in [0, n]; NULL means every L_b = n.  Keys k >= L_b are
  *     masked.  Rows q >= L_b are padding: O, dQ, dK, dV are written as 0 there
@@ -87,10 +88,15 @@ NB_API int nb_abi_version(void);
  * nb_kernel_error - report whether a kernel gave up waiting.  Every wait inside
  * the tensor-core kernels is bounded (2 s); a kernel that runs out records a
  * non-zero site code in a device word, frees its tensor memory and returns, so
- * the context stays usable (its outputs are then undefined).  This call
+ * the context stays usable (its outputs are then undefined).  The calls on the
+ * 4-bit cache record NB_KERR_* there for a token that the block table does not
+ * map.  This call
  * synchronises the current device, stores the recorded code (0 = none) in
  * *code and, when `clear` is non-zero, resets it.
  */
+#define NB_KERR_KV4_WRITE 0x51  /* nb_kv4_write skipped a token */
+#define NB_KERR_KV4_READ 0x52   /* nb_kv4_read wrote 0 for a token */
+#define NB_KERR_KV4_DECODE 0x53 /* nb_attn_kv4_decode did not see a page */
 NB_API nb_status nb_kernel_error(int* code, int clear);
 
 /*
@@ -288,6 +294,81 @@ NB_API nb_status nb_tokenize_batch(const uint8_t* seqs, const int64_t* offsets, 
  * Runs on the host only (no device, no stream, no launch).
  */
 NB_API nb_status nb_batch_ceiling(const int64_t* offsets, int batch, int k, int32_t* n_pad);
+
+#define NB_MAX_SINKS 128 /* first tokens that can stay visible */
+
+/*
+ * The 4-bit key/value cache.  A pool of pages of NB_KV4_PAGE tokens,
+ * [num_pages][kv_heads][nb_kv4_page_bytes(d)] bytes, and an int32 block table
+ * [batch][max_pages]: token t of sequence b lies in page table[b][t / 32], slot
+ * t mod 32.  A table entry outside [0, num_pages) is an unmapped page.
+ * Per token, head and group of 32 channels the cache keeps a midpoint
+ *   m = the largest bf16 <= (min + max) / 2,  a step
+ *   s = the smallest bf16 >= max(max - m, m - min) / 7.5,  and per channel a code
+ *   c = floor((x - m) / s) + 8, which stands for m + s (c - 7.5)
+ * (a group whose values are all equal to m has s = 0), so a value is off by at
+ * most s / 2.  A group that holds a non-finite value, or spans more than fp32,
+ * reads back as NaN.  (NucleoByte has no cache; sections 1-2 of its page pack
+ * bases into two bits in the same spirit.)
+ * The bytes of a page are private to the library.
+ */
+#define NB_KV4_PAGE 32
+/* Bytes of a page of one head: 2560 (d = 64) or 5120 (d = 128); 0 for another d. */
+NB_API size_t nb_kv4_page_bytes(int d);
+
+/*
+ * nb_kv4_write - quantise rows into the cache.  Token t < counts[b] of sequence b
+ * goes to position starts[b] + t.
+ * k, v         in : [batch, kv_heads, n, d] of `dtype` (NB_F32 or NB_BF16).
+ * cache        out: the pool, 16-byte aligned; only the listed tokens' bytes change.
+ * block_table  in : int32 [batch][max_pages].
+ * starts       in : int32 [batch] or NULL (all 0).
+ * counts       in : int32 [batch] or NULL (all n); values outside [0, n] are clamped.
+ * A token whose position is negative, past max_pages pages or on an unmapped
+ * page is skipped and reported (nb_kernel_error).  Two tokens of one call must
+ * not share a slot (sequences that share a page must not both write to it).
+ * batch * kv_heads * n must fit 31 bits (else NB_ERR_UNSUPPORTED).
+ */
+NB_API nb_status nb_kv4_write(const void* k, const void* v, void* cache, const int32_t* block_table,
+                              const int32_t* starts, const int32_t* counts, int batch, int kv_heads,
+                              int n, int d, int max_pages, int num_pages, int dtype, void* stream);
+
+/*
+ * nb_kv4_read - the values that the cache stands for, rounded once to `dtype`.
+ * k, v out: [batch, kv_heads, n, d]: row t < counts[b] is position starts[b] + t;
+ *           rows from counts[b] on, and unmapped positions (reported as above),
+ *           are written as 0.
+ * The other arguments as nb_kv4_write.
+ */
+NB_API nb_status nb_kv4_read(const void* cache, const int32_t* block_table, const int32_t* starts,
+                             const int32_t* counts, void* k, void* v, int batch, int kv_heads, int n,
+                             int d, int max_pages, int num_pages, int dtype, void* stream);
+
+/*
+ * nb_attn_kv4_decode - attention of the last token of each sequence over keys and
+ * values from the 4-bit cache, with a sliding window and visible first tokens
+ * (sinks): the query of sequence b has position lengths[b] - 1 and sees token
+ * k < lengths[b] when k >= lengths[b] - window or k < sinks.
+ * q           in : [batch, heads, d] bf16; heads a multiple of kv_heads.
+ * cache, block_table in: as nb_kv4_read.  Only pages that hold a visible token
+ *                  are read; the others need not be mapped.  A visible token on
+ *                  an unmapped page is not seen, and reported (nb_kernel_error).
+ * lengths     in : int32 [batch] tokens in the cache, the query's own included;
+ *                  clamped to [0, 32 max_pages]; NULL: all 32 max_pages.
+ * o           out: [batch, heads, d] bf16; 0 for an empty sequence.
+ * lse         out: [batch, heads] fp32 or NULL; -inf for an empty sequence.
+ * workspace      : device scratch of at least nb_attn_kv4_decode_workspace_size(...)
+ *                  bytes, 256-byte aligned (may be NULL when that is 0); contents
+ *                  on entry do not matter; not shared with a concurrent call.
+ * window >= 1, 0 <= sinks <= NB_MAX_SINKS.  NB_BF16 only.  Deterministic.
+ */
+NB_API size_t nb_attn_kv4_decode_workspace_size(int batch, int heads, int kv_heads, int d,
+                                                int max_pages, int window, int sinks, int dtype);
+NB_API nb_status nb_attn_kv4_decode(const void* q, const void* cache, const int32_t* block_table,
+                                    const int32_t* lengths, void* o, float* lse, void* workspace,
+                                    size_t workspace_bytes, int batch, int heads, int kv_heads,
+                                    int d, int max_pages, int num_pages, int window, int sinks,
+                                    int dtype, void* stream);
 
 #ifdef __cplusplus
 }
