@@ -13,6 +13,7 @@ from .binding import (  # noqa: F401
     attn_bwd_workspace_size,
     attn_fwd_bwd_host_workspace_size,
     attn_kv4_decode_workspace_size,
+    attn_sink_bwd_workspace_size,
     kv4_page_bytes,
     lib,
     nb_attn_bwd,
@@ -21,6 +22,8 @@ from .binding import (  # noqa: F401
     nb_attn_fwd_bwd_host,
     nb_attn_fwd_causal,
     nb_attn_kv4_decode,
+    nb_attn_sink_bwd,
+    nb_attn_sink_fwd,
     nb_batch_ceiling,
     nb_kernel_error,
     nb_kv4_read,

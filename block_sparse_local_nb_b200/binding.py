@@ -38,6 +38,9 @@ _SIGS = [
     ("nb_tokenize_kmer", _I, [_P, ctypes.c_int64, _P, _P, _I, _P]),
     ("nb_tokenize_batch", _I, [_P, _P, _I, _I, _P, _P, _I, _P]),
     ("nb_batch_ceiling", _I, [_P, _I, _I, ctypes.POINTER(ctypes.c_int32)]),
+    ("nb_attn_sink_fwd", _I, [_P] * 6 + [_I] * 8 + [_P]),
+    ("nb_attn_sink_bwd_workspace_size", ctypes.c_size_t, [_I] * 8),
+    ("nb_attn_sink_bwd", _I, [_P] * 11 + [ctypes.c_size_t] + [_I] * 8 + [_P]),
     ("nb_kv4_page_bytes", ctypes.c_size_t, [_I]),
     ("nb_kv4_write", _I, [_P] * 6 + [_I] * 7 + [_P]),
     ("nb_kv4_read", _I, [_P] * 6 + [_I] * 7 + [_P]),
@@ -190,6 +193,31 @@ def nb_batch_ceiling(offsets, batch, k=6) -> int:
     st = lib().nb_batch_ceiling(off.ctypes.data if off.size else None, batch, k, ctypes.byref(out))
     _check(st, "nb_batch_ceiling")
     return int(out.value)
+
+
+def nb_attn_sink_fwd(q, k, v, o, lse, lengths, batch, heads, kv_heads, n, d, window, sinks, dtype,
+                     stream=None, check=True):
+    st = lib().nb_attn_sink_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(lengths),
+                                batch, heads, kv_heads, n, d, window, sinks, dtype, _stream(stream))
+    if check:
+        _check(st, "nb_attn_sink_fwd")
+    return st
+
+
+def attn_sink_bwd_workspace_size(batch, heads, kv_heads, n, d, window, sinks, dtype) -> int:
+    return int(lib().nb_attn_sink_bwd_workspace_size(batch, heads, kv_heads, n, d, window, sinks,
+                                                     dtype))
+
+
+def nb_attn_sink_bwd(q, k, v, o, dout, lse, lengths, dq, dk, dv, workspace, workspace_bytes, batch,
+                     heads, kv_heads, n, d, window, sinks, dtype, stream=None, check=True):
+    st = lib().nb_attn_sink_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse),
+                                _ptr(lengths), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
+                                workspace_bytes, batch, heads, kv_heads, n, d, window, sinks, dtype,
+                                _stream(stream))
+    if check:
+        _check(st, "nb_attn_sink_bwd")
+    return st
 
 
 def kv4_page_bytes(d) -> int:

@@ -139,6 +139,31 @@ nb_status attn_bwd(const void* q, const void* k, const void* v, const void* o, c
   return e == cudaSuccess ? NB_OK : NB_ERR_CUDA;
 }
 
+// Shape checks of the attention with a window and sinks.
+nb_status check_sink(int batch, int heads, int kv_heads, int n, int d, int window, int sinks,
+                     int dtype) {
+  if (batch < 0 || heads < 0 || kv_heads < 1 || n < 0 || window < 1 || sinks < 0)
+    return NB_ERR_INVALID_ARG;
+  if (heads % kv_heads != 0) return NB_ERR_INVALID_ARG;
+  if (dtype != NB_F32 && dtype != NB_BF16) return NB_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || dtype != NB_BF16 || sinks > NB_MAX_SINKS) return NB_ERR_UNSUPPORTED;
+  if (heads > 65535 || batch > 65535) return NB_ERR_UNSUPPORTED;
+  // work items and the blocks of the row statistics fit 31 bits
+  const double rows = static_cast<double>(batch) * heads * (static_cast<double>(n) + 127);
+  if (rows > 3.0e10 || n > INT32_MAX - 512) return NB_ERR_UNSUPPORTED;
+  return NB_OK;
+}
+
+nb::SinkArgs make_sink(const void* q, const void* k, const void* v, const void* o,
+                       const void* dout, const float* lse, const int32_t* lengths, void* dq,
+                       void* dk, void* dv, void* ws, int batch, int heads, int kv_heads, int n,
+                       int d, int window, int sinks) {
+  nb::SinkArgs a = {q, k, v, o, dout, const_cast<float*>(lse), lengths, dq, dk, dv, ws, nullptr,
+                    batch, heads, kv_heads, n, d, window, sinks,
+                    static_cast<float>(1.0 / sqrt(static_cast<double>(d)))};
+  return a;
+}
+
 // Shape checks of the 4-bit cache calls.  Positions, rows and grid sizes fit 31 bits.
 nb_status check_kv4(int batch, int kv_heads, int d, int max_pages, int num_pages) {
   if (batch < 0 || kv_heads < 1 || max_pages < 0 || num_pages < 0) return NB_ERR_INVALID_ARG;
@@ -314,6 +339,56 @@ nb_status nb_batch_ceiling(const int64_t* offsets, int batch, int k, int32_t* n_
   if (ceil32 > INT32_MAX) return NB_ERR_INVALID_ARG;
   *n_pad = static_cast<int32_t>(ceil32);
   return NB_OK;
+}
+
+nb_status nb_attn_sink_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
+                           const int32_t* lengths, int batch, int heads, int kv_heads, int n, int d,
+                           int window, int sinks, int dtype, void* stream) {
+  nb_status st = check_sink(batch, heads, kv_heads, n, d, window, sinks, dtype);
+  if (st != NB_OK) return st;
+  if (batch == 0 || heads == 0 || n == 0) return NB_OK;
+  if (!q || !k || !v || !o) return NB_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) ||
+      !aligned4(lengths))
+    return NB_ERR_MISALIGNED;
+  st = check_device();
+  if (st != NB_OK) return st;
+  nb::SinkArgs a = make_sink(q, k, v, o, nullptr, lse, lengths, nullptr, nullptr, nullptr, nullptr,
+                             batch, heads, kv_heads, n, d, window, sinks);
+  a.err = error_word();
+  const cudaError_t e = nb::launch_attn_sink_fwd(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? NB_OK : NB_ERR_CUDA;
+}
+
+size_t nb_attn_sink_bwd_workspace_size(int batch, int heads, int kv_heads, int n, int d, int window,
+                                       int sinks, int dtype) {
+  if (check_sink(batch, heads, kv_heads, n, d, window, sinks, dtype) != NB_OK) return 0;
+  if (batch == 0 || heads == 0 || n == 0) return 0;
+  return nb::sink_bwd_workspace_bytes(make_sink(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
+                                                nullptr, nullptr, nullptr, nullptr, nullptr, batch,
+                                                heads, kv_heads, n, d, window, sinks));
+}
+
+nb_status nb_attn_sink_bwd(const void* q, const void* k, const void* v, const void* o,
+                           const void* dout, const float* lse, const int32_t* lengths, void* dq,
+                           void* dk, void* dv, void* workspace, size_t workspace_bytes, int batch,
+                           int heads, int kv_heads, int n, int d, int window, int sinks, int dtype,
+                           void* stream) {
+  nb_status st = check_sink(batch, heads, kv_heads, n, d, window, sinks, dtype);
+  if (st != NB_OK) return st;
+  if (batch == 0 || heads == 0 || n == 0) return NB_OK;
+  st = bwd_pointers(q, k, v, o, dout, lse, lengths, dq, dk, dv);
+  if (st != NB_OK) return st;
+  nb::SinkArgs a = make_sink(q, k, v, o, dout, lse, lengths, dq, dk, dv, workspace, batch, heads,
+                             kv_heads, n, d, window, sinks);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      workspace_bytes < nb::sink_bwd_workspace_bytes(a))
+    return NB_ERR_WORKSPACE;
+  st = check_device();
+  if (st != NB_OK) return st;
+  a.err = error_word();
+  const cudaError_t e = nb::launch_attn_sink_bwd(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? NB_OK : NB_ERR_CUDA;
 }
 
 size_t nb_kv4_page_bytes(int d) {

@@ -1,0 +1,905 @@
+// Causal attention with a sliding window and visible first tokens (sinks),
+// backward, on the 5th-generation tensor cores (tcgen05 + TMEM), bf16 in / fp32
+// accumulate.  With P recomputed from the stored log-sum-exp and
+// D_i = sum_k dO_ik O_ik:
+//   dS = P (dO V^T - D),  dV = P^T dO,  dK = dS^T Q / sqrt(d),  dQ = dS K / sqrt(d),
+// dK and dV summed over the query heads that share a key/value head.
+//
+// Four launches on the caller's stream:
+//   rows   per query row -D and -lse log2(e) into the workspace (-inf past the
+//          length, so P is 0 there), and zeros for gradient tiles past it;
+//   main   <kDQ = false>: a 128-key tile of K and V stays, 64-query chunks of Q
+//          and dO stream past: S^T = K Q^T, dP^T = V dO^T (keys on the lanes),
+//          dV += P^T dO, dK += dS^T Q;
+//   main   <kDQ = true>: a 128-query tile of Q and dO stays, 64-key chunks of K
+//          and V stream past: S = Q K^T, dP = dO V^T, dQ += dS K;
+//   join   adds the parts of key tiles that were split (below).
+// S and dP are computed twice (7 products instead of 5), but every gradient is
+// accumulated in tensor memory in a fixed order: no fp32 accumulator of dQ in
+// global memory (cleared, added to with atomics and read back), and results
+// that repeat bit for bit.  P and dS overwrite S and dP in tensor memory and are
+// the A operands of the gradient products from there; neither passes through
+// shared memory.  Both are rounded to bf16 as operands.
+//
+// The first key tile holds the sinks, which every later query of every head of
+// the group sees: up to group * n / 64 chunks against group * (window + 128) / 64
+// for another tile.  A tile's chunks are therefore cut into parts when they
+// exceed an SM's even share; parts are fp32 tiles in the workspace that the last
+// launch adds in order.
+//
+// Warp roles (512 threads, four warpgroups with reallocated registers): warp 0
+// TMA producer (a chunk that reaches past the length lands on a barrier of its
+// own, and the warp zeroes the rows past it: P is 0 there, but 0 x NaN is not);
+// warp 1 TMEM owner and S/dP issuer; warp 2 issuer of the gradient products;
+// warpgroups 1 and 2 take the chunks in turn (thread = lane, 64 columns);
+// warpgroup 3 epilogue (thread = lane), staging through swizzled shared memory
+// and TMA tensor stores.  Every wait is bounded (sm100.cuh).
+#include <math.h>
+
+#include "nb_internal.h"
+#include "sm100.cuh"
+
+namespace nb {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 512;
+constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+constexpr int kRows = 128;                // rows of the tile that stays
+constexpr int kChunk = 64;                // rows of a streamed chunk
+constexpr int kSlab = kRows * 128;        // swizzled box of the tile: 128 rows x 64 bf16
+constexpr int kChunkSlab = kChunk * 128;  // of a chunk
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMaxBatch = 1024;           // sequences in the shared-memory work table
+
+struct Params {
+  const void* o;
+  const void* dout;
+  const float* lse;
+  const int32_t* lengths;
+  void* dq;
+  void* dk;
+  void* dv;
+  float* nd;     // [batch * heads][npad]: -D
+  float* nlse2;  // [batch * heads][npad]: -lse log2(e)
+  float* part0;  // parts of the first key tiles, [batch * kv_heads][s0][dV, dK][128][d]
+  float* part1;  // parts of the others, [batch * kv_heads][ntiles - 1][s1][dV, dK][128][d]
+  int* err;
+  int batch, heads, kv_heads, group, n, npad, ntiles, window, sinks;
+  int s0, s1;    // parts of the first key tile, of another
+  int items;     // of the main kernel
+  float scale;
+};
+
+__device__ __forceinline__ int length_of(const Params& p, int b) {
+  const int L = p.lengths ? p.lengths[b] : p.n;
+  return min(max(L, 0), p.n);
+}
+
+// Chunks of queries that see key tile `tile` (per head), in a sequence of length L > 128 tile.
+__host__ __device__ __forceinline__ int query_chunks(int tile, int L, int window, int sinks) {
+  const int k0 = tile * kRows;
+  // the last key of the tile is seen up to its window's end, the sinks by every query
+  const int64_t far = static_cast<int64_t>(k0) + kRows - 1 + window;
+  const int end = (tile == 0 && sinks > 0) || far > L ? L : static_cast<int>(far);
+  return (end - k0 + kChunk - 1) / kChunk;
+}
+
+template <int D, bool kDQ>
+struct Cfg {
+  // tiles that stay: two buffers at d = 64 (the next item's loads overlap), one at d = 128
+  static constexpr int NT = D == 64 ? 2 : 1;
+  static constexpr int NS = D == 64 ? 6 : 3;  // chunk stages
+  static constexpr int NSB = 2;               // S/dP buffers in tensor memory
+  static constexpr int NOUT = kDQ ? 1 : 2;    // gradients of an item
+  static constexpr int NACC = D == 64 || kDQ ? 2 : 1;  // accumulator sets
+  static constexpr int kTile = kRows * D * 2;
+  static constexpr int kHalf = kChunk * D * 2;   // one of the chunk's two operands
+  static constexpr int oTile = 0;                // buffer i: X at oTile + 2 i kTile, Y after it
+  static constexpr int oCh = oTile + NT * 2 * kTile;  // stage s: X at oCh + 2 s kHalf, Y after it
+  static constexpr int oStg = oCh + NS * 2 * kHalf;   // output staging, one tile
+  static constexpr int oCol = oStg + kTile;           // stage s: -lse log2 e and -D of its columns
+  static constexpr int oBar = oCol + (kDQ ? 0 : NS * 2 * kChunk * 4);
+  static constexpr int bTFull = 0, bTFree = bTFull + NT, bCFull = bTFree + NT, bCFree = bCFull + NS,
+                       bSFull = bCFree + NS, bSFree = bSFull + NSB, bPFull = bSFree + NSB,
+                       bAFull = bPFull + NSB, bAFree = bAFull + NACC, bFix = bAFree + NACC,
+                       bDone = bFix + 1, nBar = bDone + 1;
+  static constexpr int oSlot = oBar + nBar * 8;
+  static constexpr int oPre = oSlot + 16;             // work table: pre[0..batch], len[0..batch)
+  static constexpr int kSmem = oPre + (2 * kMaxBatch + 1) * 4 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  static constexpr uint32_t kTmemCols = 512;
+  // accumulators first, then the S/dP buffers (64 + 64 columns each)
+  __device__ static constexpr uint32_t tAcc(int acc, int out) { return (acc * NOUT + out) * D; }
+  static constexpr uint32_t tS0 = NACC * NOUT * D;
+  __device__ static constexpr uint32_t tS(int sb) { return tS0 + sb * 2 * kChunk; }
+  static_assert(tS0 + NSB * 2 * kChunk <= kTmemCols, "tensor memory columns");
+  static constexpr int kRegsCtl = 72;
+  static constexpr int kRegsGrad = 168;
+  static constexpr int kRegsEpi = 104;
+  static_assert(128 * (kRegsCtl + 2 * kRegsGrad + kRegsEpi) <= kThreads * kLaunchRegs,
+                "register budget");
+};
+
+struct Item {
+  int b, h, tile, L;  // h: query head (kDQ) or key/value head
+  int c0, nch;        // first chunk and number of chunks
+  int nq;             // chunks per head (key tiles)
+  int k0, far;        // kDQ: first key of the window's chunks, chunks of sinks before them
+  int part, parts;    // key tiles: this item's part
+};
+
+template <bool kDQ>
+__device__ __forceinline__ int items_of(const Params& p, int L) {
+  const int t = (L + kRows - 1) / kRows;
+  if (kDQ) return p.heads * t;
+  return t == 0 ? 0 : p.kv_heads * (p.s0 + (t - 1) * p.s1);
+}
+
+// Warp-cooperative: prefix sums of the items per sequence, and the lengths.
+template <bool kDQ>
+__device__ void build_table(int* pre, const Params& p, int lane) {
+  if (p.batch > kMaxBatch) return;
+  int carry = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const int b = b0 + lane;
+    int v = 0;
+    if (b < p.batch) {
+      const int L = length_of(p, b);
+      pre[kMaxBatch + 1 + b] = L;
+      v = items_of<kDQ>(p, L);
+    }
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, v, off);
+      if (lane >= off) v += t;
+    }
+    if (b < p.batch) pre[b + 1] = carry + v;
+    carry += __shfl_sync(0xffffffffu, v, 31);
+  }
+  if (lane == 0) pre[0] = 0;
+}
+
+__device__ __forceinline__ int item_count(const Params& p, const int* pre) {
+  return p.batch <= kMaxBatch ? pre[p.batch] : p.items;
+}
+
+// This CTA's item of round r; every second round runs backwards over the CTAs.
+__device__ __forceinline__ int item_at(int r) {
+  const int c = static_cast<int>(blockIdx.x), g = static_cast<int>(gridDim.x);
+  return r * g + ((r & 1) ? g - 1 - c : c);
+}
+
+// Item k.  Heads are innermost; query tiles run from the last (most keys) to the
+// first, key tiles from the first (the sinks' parts).
+template <bool kDQ>
+__device__ __forceinline__ Item item(const Params& p, const int* pre, int k) {
+  Item x;
+  int rem;
+  if (p.batch <= kMaxBatch) {
+    int lo = 0, hi = p.batch - 1;  // largest b with pre[b] <= k
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= k) lo = mid; else hi = mid - 1;
+    }
+    x.b = lo;
+    rem = k - pre[lo];
+    x.L = pre[kMaxBatch + 1 + lo];
+  } else {
+    const int per = p.items / p.batch;
+    x.b = k / per;
+    rem = k - x.b * per;
+    x.L = length_of(p, x.b);
+  }
+  const int heads = kDQ ? p.heads : p.kv_heads;
+  const int slot = rem / heads;
+  x.h = rem - slot * heads;
+  x.c0 = x.nch = x.nq = x.k0 = x.far = x.part = 0;
+  x.parts = 1;
+  if (kDQ) {
+    x.tile = (p.batch <= kMaxBatch ? (x.L + kRows - 1) / kRows : p.ntiles) - 1 - slot;
+    const int q0 = x.tile * kRows;
+    if (q0 >= x.L) return x;
+    x.k0 = q0 >= p.window ? q0 - p.window + 1 : 0;
+    if (p.sinks > 0 && x.k0 > 0) {
+      const int f = (p.sinks + kChunk - 1) / kChunk;
+      if (x.k0 <= f * kChunk) x.k0 = 0;  // as many chunks either way
+      else x.far = f;
+    }
+    x.nch = x.far + (min(q0 + kRows, x.L) - x.k0 + kChunk - 1) / kChunk;
+  } else {
+    if (slot < p.s0) {
+      x.tile = 0;
+      x.part = slot;
+      x.parts = p.s0;
+    } else {
+      const int t = (slot - p.s0) / p.s1;
+      x.tile = 1 + t;
+      x.part = slot - p.s0 - t * p.s1;
+      x.parts = p.s1;
+    }
+    if (x.tile * kRows >= x.L) return x;
+    x.nq = query_chunks(x.tile, x.L, p.window, p.sinks);
+    const int64_t all = static_cast<int64_t>(x.nq) * p.group;
+    x.c0 = static_cast<int>(all * x.part / x.parts);
+    x.nch = static_cast<int>(all * (x.part + 1) / x.parts) - x.c0;
+  }
+  return x;
+}
+
+// Chunk c of an item: its first row and the head it belongs to.
+struct Chunk {
+  int row, bh;
+};
+template <bool kDQ>
+__device__ __forceinline__ Chunk chunk(const Params& p, const Item& x, int c) {
+  Chunk k;
+  if (kDQ) {
+    k.row = c < x.far ? c * kChunk : x.k0 + (c - x.far) * kChunk;
+    k.bh = x.b * p.kv_heads + x.h / p.group;
+  } else {
+    const int j = x.c0 + c, g = j / x.nq;
+    k.row = x.tile * kRows + (j - g * x.nq) * kChunk;
+    k.bh = x.b * p.heads + x.h * p.group + g;
+  }
+  return k;
+}
+
+enum : int { kErrTFree = 0x81, kErrCFree, kErrFix, kErrTFull, kErrCFull, kErrSFree, kErrPFull,
+             kErrAFree, kErrSFull, kErrGCFull, kErrAFull, kErrDone };
+
+// Tiles and chunks (warp 0, the whole warp; lane 0 issues).
+template <int D, bool kDQ>
+__device__ int producer(const Params& p, const int* pre, uint32_t base, uint8_t* gbase, int lane,
+                        const CUtensorMap* tx, const CUtensorMap* ty, const CUtensorMap* cx,
+                        const CUtensorMap* cy) {
+  using C = Cfg<D, kDQ>;
+  const uint32_t bar = base + C::oBar;
+  const int count = item_count(p, pre);
+  int g = 0, tc = 0, fixes = 0;
+  for (int rd = 0, it; (it = item_at(rd)) < count; ++rd) {
+    const Item x = item<kDQ>(p, pre, it);
+    if (x.nch == 0) continue;
+    const int tb = tc % C::NT;
+    bool ok = true;
+    if (lane == 0) {
+      ok = mbar_wait(bar + 8 * (C::bTFree + tb), ((tc / C::NT) & 1) ^ 1);
+      if (ok) {
+        const uint32_t full = bar + 8 * (C::bTFull + tb);
+        mbar_arrive_expect_tx(full, 2 * C::kTile);
+        const uint32_t s = base + C::oTile + tb * 2 * C::kTile;
+        const int bh = x.b * (kDQ ? p.heads : p.kv_heads) + x.h;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          tma_load_3d(s + i * kSlab, tx, full, i * 64, x.tile * kRows, bh);
+          tma_load_3d(s + C::kTile + i * kSlab, ty, full, i * 64, x.tile * kRows, bh);
+        }
+      }
+    }
+    if (!__all_sync(0xffffffffu, ok)) return kErrTFree;
+    for (int c = 0; c < x.nch; ++c) {
+      const int G = g + c, st = G % C::NS;
+      const Chunk k = chunk<kDQ>(p, x, c);
+      const bool fix = k.row + kChunk > x.L && x.L < p.n;  // rows past the length hold other data
+      const uint32_t full = bar + 8 * (C::bCFull + st);
+      const uint32_t land = fix ? bar + 8 * C::bFix : full;
+      const uint32_t s = base + C::oCh + st * 2 * C::kHalf;
+      if (lane == 0) {
+        ok = mbar_wait(bar + 8 * (C::bCFree + st), ((G / C::NS) & 1) ^ 1);
+        if (ok) {
+          mbar_arrive_expect_tx(land, 2 * C::kHalf + (kDQ ? 0 : 2 * kChunk * 4));
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) {
+            tma_load_3d(s + i * kChunkSlab, cx, land, i * 64, k.row, k.bh);
+            tma_load_3d(s + C::kHalf + i * kChunkSlab, cy, land, i * 64, k.row, k.bh);
+          }
+          if (!kDQ) {  // the columns' statistics, padded to whole tiles of 128
+            const int64_t at = static_cast<int64_t>(k.bh) * p.npad + k.row;
+            const uint32_t sc = base + C::oCol + st * 2 * kChunk * 4;
+            bulk_load(sc, p.nlse2 + at, kChunk * 4, land);
+            bulk_load(sc + kChunk * 4, p.nd + at, kChunk * 4, land);
+          }
+        }
+      }
+      if (!__all_sync(0xffffffffu, ok)) return kErrCFree;
+      if (fix) {
+        if (!__all_sync(0xffffffffu, mbar_wait(land, fixes & 1))) return kErrFix;
+        ++fixes;
+        uint4* v = reinterpret_cast<uint4*>(gbase + C::oCh + st * 2 * C::kHalf);
+        // whole 128-byte rows of every box, so the swizzle does not matter
+        for (int i = 0; i < 2 * (D / 64); ++i)
+          for (int j = (x.L - k.row) * 8 + lane; j < kChunk * 8; j += 32)
+            v[i * (kChunkSlab / 16) + j] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
+      }
+    }
+    g += x.nch;
+    ++tc;
+  }
+  return 0;
+}
+
+// S and dP of every chunk (warp 1, one thread).
+template <int D, bool kDQ>
+__device__ int s_issuer(const Params& p, const int* pre, uint32_t base, uint32_t tmem) {
+  using C = Cfg<D, kDQ>;
+  const uint32_t bar = base + C::oBar;
+  constexpr uint32_t kId = idesc_bf16_f32(128, kChunk, false, false);
+  const int count = item_count(p, pre);
+  int g = 0, tc = 0;
+  for (int rd = 0, it; (it = item_at(rd)) < count; ++rd) {
+    const Item x = item<kDQ>(p, pre, it);
+    if (x.nch == 0) continue;
+    const int tb = tc % C::NT;
+    const uint32_t sT = base + C::oTile + tb * 2 * C::kTile;
+    const uint64_t dX = smem_desc_sw128(sT, 0, 1024), dY = smem_desc_sw128(sT + C::kTile, 0, 1024);
+    if (!mbar_wait(bar + 8 * (C::bTFull + tb), (tc / C::NT) & 1)) return kErrTFull;
+    for (int c = 0; c < x.nch; ++c) {
+      const int G = g + c, st = G % C::NS, sb = G % C::NSB;
+      const uint32_t sC = base + C::oCh + st * 2 * C::kHalf;
+      const uint64_t eX = smem_desc_sw128(sC, 0, 1024), eY = smem_desc_sw128(sC + C::kHalf, 0, 1024);
+      if (!mbar_wait(bar + 8 * (C::bCFull + st), (G / C::NS) & 1)) return kErrCFull;
+      if (!mbar_wait(bar + 8 * (C::bSFree + sb), ((G / C::NSB) & 1) ^ 1)) return kErrSFree;
+      tc_fence_after();
+      const uint32_t tS = tmem + C::tS(sb);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t ot = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
+        const uint32_t oc = ((k >> 2) * kChunkSlab + (k & 3) * 32) >> 4;
+        mma_bf16_ss(tS, desc_add(dX, ot), desc_add(eX, oc), kId, k > 0);
+      }
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t ot = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
+        const uint32_t oc = ((k >> 2) * kChunkSlab + (k & 3) * 32) >> 4;
+        mma_bf16_ss(tS + kChunk, desc_add(dY, ot), desc_add(eY, oc), kId, k > 0);
+      }
+      mma_commit(bar + 8 * (C::bSFull + sb));
+      if (c == x.nch - 1) mma_commit(bar + 8 * (C::bTFree + tb));  // the tile's only readers
+    }
+    g += x.nch;
+    ++tc;
+  }
+  return 0;
+}
+
+// The gradient products of every chunk (warp 2, one thread): A = P or dS from
+// tensor memory, B = the chunk's rows (MN-major: 64-column atoms kChunkSlab
+// apart, 16 rows = 2048 bytes per step).
+template <int D, bool kDQ>
+__device__ int grad_issuer(const Params& p, const int* pre, uint32_t base, uint32_t tmem) {
+  using C = Cfg<D, kDQ>;
+  const uint32_t bar = base + C::oBar;
+  constexpr uint32_t kId = idesc_bf16_f32(128, D, false, true);
+  const int count = item_count(p, pre);
+  int g = 0, tc = 0;
+  for (int rd = 0, it; (it = item_at(rd)) < count; ++rd) {
+    const Item x = item<kDQ>(p, pre, it);
+    if (x.nch == 0) continue;
+    const int acc = tc % C::NACC;
+    for (int c = 0; c < x.nch; ++c) {
+      const int G = g + c, st = G % C::NS, sb = G % C::NSB;
+      const uint32_t sC = base + C::oCh + st * 2 * C::kHalf;
+      const uint64_t eX = smem_desc_sw128(sC, kChunkSlab, 1024);
+      const uint64_t eY = smem_desc_sw128(sC + C::kHalf, kChunkSlab, 1024);
+      if (c == 0 && !mbar_wait(bar + 8 * (C::bAFree + acc), ((tc / C::NACC) & 1) ^ 1))
+        return kErrAFree;
+      if (!mbar_wait(bar + 8 * (C::bPFull + sb), (G / C::NSB) & 1)) return kErrPFull;
+      tc_fence_after();
+      const uint32_t tP = tmem + C::tS(sb), tDS = tP + kChunk;
+      const uint32_t out0 = tmem + C::tAcc(acc, 0);
+      if (kDQ) {  // dQ += dS K
+#pragma unroll
+        for (int k = 0; k < kChunk / 16; ++k)
+          mma_bf16_ts(out0, tDS + 8 * k, desc_add(eX, (k * 2048) >> 4), kId, c > 0 || k > 0);
+      } else {    // dV += P^T dO, dK += dS^T Q
+        const uint32_t out1 = tmem + C::tAcc(acc, C::NOUT - 1);
+#pragma unroll
+        for (int k = 0; k < kChunk / 16; ++k)
+          mma_bf16_ts(out0, tP + 8 * k, desc_add(eY, (k * 2048) >> 4), kId, c > 0 || k > 0);
+#pragma unroll
+        for (int k = 0; k < kChunk / 16; ++k)
+          mma_bf16_ts(out1, tDS + 8 * k, desc_add(eX, (k * 2048) >> 4), kId, c > 0 || k > 0);
+      }
+      mma_commit(bar + 8 * (C::bSFree + sb));
+      mma_commit(bar + 8 * (C::bCFree + st));
+      if (c == x.nch - 1) mma_commit(bar + 8 * (C::bAFull + acc));
+    }
+    g += x.nch;
+    ++tc;
+  }
+  return 0;
+}
+
+// Bits [lo, hi) of a 64-bit word (clipped to it).
+__device__ __forceinline__ uint64_t bit_range(int64_t lo, int64_t hi) {
+  const int a = static_cast<int>(lo < 0 ? 0 : (lo > 64 ? 64 : lo));
+  const int b = static_cast<int>(hi < 0 ? 0 : (hi > 64 ? 64 : hi));
+  return b > a ? (~0ull >> (64 - (b - a))) << a : 0ull;
+}
+
+// P and dS of the chunks of one warpgroup (every second chunk), thread = lane r.
+template <int D, bool kDQ>
+__device__ int grad_warps(const Params& p, const int* pre, uint32_t base, uint8_t* gbase,
+                          uint32_t tmem, int wg, int wq, int lane) {
+  using C = Cfg<D, kDQ>;
+  const uint32_t bar = base + C::oBar;
+  const int r = wq * 32 + lane;
+  const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+  const float sl2 = p.scale * kLog2e;
+  auto all_ok = [](bool ok) { return __all_sync(0xffffffffu, ok); };
+  const int count = item_count(p, pre);
+  int g = 0;
+  for (int rd = 0, it; (it = item_at(rd)) < count; ++rd) {
+    const Item x = item<kDQ>(p, pre, it);
+    if (x.nch == 0) continue;
+    const int row = x.tile * kRows + r;  // key (or query, kDQ) of this lane
+    float nl_row = 0.f, nd_row = 0.f;
+    if (kDQ) {
+      const int64_t at = (static_cast<int64_t>(x.b) * p.heads + x.h) * p.npad + row;
+      nl_row = p.nlse2[at];
+      nd_row = p.nd[at];
+    }
+    for (int c = (g & 1) ^ wg; c < x.nch; c += 2) {
+      const int G = g + c, st = G % C::NS, sb = G % C::NSB;
+      const int col = chunk<kDQ>(p, x, c).row;  // first column's query (or key, kDQ)
+      const int t0 = x.tile * kRows;
+      bool whole;
+      uint64_t mask = ~0ull;
+      if (kDQ) {
+        whole = c >= x.far && col + kChunk - 1 <= t0 && col > t0 + kRows - 1 - p.window &&
+                t0 + kRows <= x.L;
+        if (!whole) {
+          const int first = row >= p.window ? row - p.window + 1 : 0;
+          if (c < x.far) mask = bit_range(0, p.sinks - col);
+          else mask = bit_range(first - col, row + 1 - col) |
+                      (x.far ? 0ull : bit_range(0, min(p.sinks, row + 1) - col));
+          if (row >= x.L) mask = 0ull;
+        }
+      } else {
+        whole = col >= t0 + kRows - 1 && col - t0 < p.window - (kChunk - 1) &&
+                col + kChunk <= x.L;  // then the keys, which come before col, are below L too
+        if (!whole) {
+          const int64_t end = row < p.sinks ? x.L : static_cast<int64_t>(row) + p.window;
+          mask = row < x.L ? bit_range(row - col, (end < x.L ? end : x.L) - col) : 0ull;
+        }
+      }
+      if (!kDQ && !all_ok(mbar_wait(bar + 8 * (C::bCFull + st), (G / C::NS) & 1)))
+        return kErrGCFull;
+      if (!all_ok(mbar_wait(bar + 8 * (C::bSFull + sb), (G / C::NSB) & 1))) return kErrSFull;
+      tc_fence_after();
+      const float* nl = reinterpret_cast<const float*>(gbase + C::oCol + st * 2 * kChunk * 4);
+      const float* nd = nl + kChunk;
+      const float2 sl = make_float2(sl2, sl2);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {  // 32 columns at a time
+        uint32_t wp[16], ws[16];
+        const uint32_t mw = static_cast<uint32_t>(mask >> (32 * j));
+        if (whole || __any_sync(0xffffffffu, mw != 0u)) {
+          float s[32], dp[32];
+          tmem_ld32(trow + C::tS(sb) + 32 * j, s);
+          tmem_ld32(trow + C::tS(sb) + kChunk + 32 * j, dp);
+          tmem_wait_ld();
+          reg_fence(s);
+          reg_fence(dp);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {  // pairs of columns, packed fp32x2 arithmetic
+            float2 n2, d2;
+            if (kDQ) {
+              n2 = make_float2(nl_row, nl_row);
+              d2 = make_float2(nd_row, nd_row);
+            } else {
+              n2 = *reinterpret_cast<const float2*>(nl + 32 * j + 2 * i);
+              d2 = *reinterpret_cast<const float2*>(nd + 32 * j + 2 * i);
+            }
+            const float2 e = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), sl, n2);
+            float2 pe = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+            float2 de = __fmul2_rn(pe, __fadd2_rn(make_float2(dp[2 * i], dp[2 * i + 1]), d2));
+            if (!whole) {  // selects, not products: a masked place may hold anything
+              const bool v0 = (mw >> (2 * i)) & 1u, v1 = (mw >> (2 * i + 1)) & 1u;
+              pe.x = v0 ? pe.x : 0.f;
+              pe.y = v1 ? pe.y : 0.f;
+              de.x = v0 ? de.x : 0.f;
+              de.y = v1 ? de.y : 0.f;
+            }
+            wp[i] = pack_bf16(pe.x, pe.y);
+            ws[i] = pack_bf16(de.x, de.y);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) wp[i] = ws[i] = 0u;
+        }
+        // P and dS over the S and dP columns already read: columns 16 j .. 16 j + 15
+        if (!kDQ) tmem_st16u(trow + C::tS(sb) + 16 * j, wp);
+        tmem_st16u(trow + C::tS(sb) + kChunk + 16 * j, ws);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar + 8 * (C::bPFull + sb));
+    }
+    g += x.nch;
+  }
+  return 0;
+}
+
+// Gradients of finished items (warpgroup 3, thread = lane r): bf16 tiles through
+// the staging buffer and a TMA store, or fp32 parts straight to the workspace.
+template <int D, bool kDQ>
+__device__ int epi_warps(const Params& p, const int* pre, uint32_t base, uint8_t* gbase,
+                         uint32_t tmem, int wq, int lane, const CUtensorMap* to0,
+                         const CUtensorMap* to1) {
+  using C = Cfg<D, kDQ>;
+  const uint32_t bar = base + C::oBar;
+  const int r = wq * 32 + lane;
+  const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+  const bool leader = r == 0;
+  auto all_ok = [](bool ok) { return __all_sync(0xffffffffu, ok); };
+  const int count = item_count(p, pre);
+  int tc = 0;
+  for (int rd = 0, it; (it = item_at(rd)) < count; ++rd) {
+    const Item x = item<kDQ>(p, pre, it);
+    if (x.nch == 0) continue;
+    const int acc = tc % C::NACC;
+    if (!all_ok(mbar_wait(bar + 8 * (C::bAFull + acc), (tc / C::NACC) & 1))) return kErrAFull;
+    tc_fence_after();
+    const bool valid = x.tile * kRows + r < x.L;
+    const int bh = x.b * (kDQ ? p.heads : p.kv_heads) + x.h;
+    float* part = nullptr;
+    if (!kDQ && x.parts > 1) {
+      const int64_t slot =
+          x.tile == 0 ? static_cast<int64_t>(bh) * p.s0 + x.part
+                      : (static_cast<int64_t>(bh) * (p.ntiles - 1) + x.tile - 1) * p.s1 + x.part;
+      part = (x.tile == 0 ? p.part0 : p.part1) + slot * 2 * kRows * D + r * D;
+    }
+#pragma unroll
+    for (int out = 0; out < C::NOUT; ++out) {
+      const float mul = kDQ || out == 1 ? p.scale : 1.f;  // dQ, dK; dV
+      if (part == nullptr) {
+        if (leader) bulk_wait_read0();  // the previous store is done with the staging
+        named_barrier(2, 128);
+      }
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        float v[32];
+        tmem_ld32(trow + C::tAcc(acc, out) + 32 * j, v);
+        tmem_wait_ld();
+        reg_fence(v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = valid ? v[i] * mul : 0.f;
+        if (part != nullptr) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(part + out * kRows * D + 32 * j + 4 * i) =
+                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int gc = 4 * j + u;  // 16-byte chunk of the output row
+            *reinterpret_cast<uint4*>(gbase + C::oStg + (gc >> 3) * kSlab + r * 128 +
+                                      (((gc & 7) ^ (r & 7)) << 4)) =
+                make_uint4(pack_bf16(v[8 * u], v[8 * u + 1]), pack_bf16(v[8 * u + 2], v[8 * u + 3]),
+                           pack_bf16(v[8 * u + 4], v[8 * u + 5]),
+                           pack_bf16(v[8 * u + 6], v[8 * u + 7]));
+          }
+        }
+      }
+      if (out == C::NOUT - 1) {
+        tc_fence_before();
+        mbar_arrive(bar + 8 * (C::bAFree + acc));
+      }
+      if (part == nullptr) {
+        fence_proxy_async_smem();
+        named_barrier(1, 128);
+        if (leader) {
+#pragma unroll
+          for (int s = 0; s < D / 64; ++s)
+            tma_store_3d(out == 0 ? to0 : to1, base + C::oStg + s * kSlab, s * 64, x.tile * kRows,
+                         bh);
+          bulk_commit();
+        }
+      }
+    }
+    ++tc;
+  }
+  if (leader) bulk_wait_all0();
+  return 0;
+}
+
+// tx, ty: the tile that stays (K, V or Q, dO); cx, cy: the chunks (Q, dO or K, V);
+// to0, to1: dV, dK or dQ twice.
+template <int D, bool kDQ>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_sink_bwd_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty,
+                         const __grid_constant__ CUtensorMap cx, const __grid_constant__ CUtensorMap cy,
+                         const __grid_constant__ CUtensorMap to0,
+                         const __grid_constant__ CUtensorMap to1, const Params p) {
+  using C = Cfg<D, kDQ>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t bar = base + C::oBar;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NT; ++i) {
+      mbar_init(bar + 8 * (C::bTFull + i), 1);
+      mbar_init(bar + 8 * (C::bTFree + i), 1);
+    }
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(bar + 8 * (C::bCFull + i), 1);
+      mbar_init(bar + 8 * (C::bCFree + i), 1);
+    }
+    for (int i = 0; i < C::NSB; ++i) {
+      mbar_init(bar + 8 * (C::bSFull + i), 1);
+      mbar_init(bar + 8 * (C::bSFree + i), 1);
+      mbar_init(bar + 8 * (C::bPFull + i), 128);
+    }
+    for (int i = 0; i < C::NACC; ++i) {
+      mbar_init(bar + 8 * (C::bAFull + i), 1);
+      mbar_init(bar + 8 * (C::bAFree + i), 128);
+    }
+    mbar_init(bar + 8 * C::bFix, 1);
+    mbar_init(bar + 8 * C::bDone, 2);  // one commit per MMA-issuing thread
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tx);
+    prefetch_tmap(&ty);
+    prefetch_tmap(&cx);
+    prefetch_tmap(&cy);
+    prefetch_tmap(&to0);
+    prefetch_tmap(&to1);
+  }
+  if (warp == 1) {
+    tmem_alloc(base + C::oSlot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_wait();  // everything above overlaps the previous kernel's tail
+  int* pre = reinterpret_cast<int*>(gbase + C::oPre);
+  if (warp == 0) build_table<kDQ>(pre, p, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + C::oSlot);
+
+  int err = 0;
+  if (warp < 4) {
+    regs_dec<C::kRegsCtl, kLaunchRegs>();
+    if (warp == 0) err = producer<D, kDQ>(p, pre, base, gbase, lane, &tx, &ty, &cx, &cy);
+    if (warp == 1 && lane == 0) err = s_issuer<D, kDQ>(p, pre, base, tmem);
+    if (warp == 2 && lane == 0) err = grad_issuer<D, kDQ>(p, pre, base, tmem);
+  } else if (warp < 12) {
+    regs_inc<C::kRegsGrad, kLaunchRegs>();
+    err = grad_warps<D, kDQ>(p, pre, base, gbase, tmem, (warp - 4) >> 2, warp & 3, lane);
+  } else {
+    regs_dec<C::kRegsEpi, kLaunchRegs>();
+    err = epi_warps<D, kDQ>(p, pre, base, gbase, tmem, warp & 3, lane, &to0, &to1);
+  }
+  if (err) record_error(p.err, err);
+
+  pdl_trigger();
+  __syncthreads();
+  if (warp == 2 && lane == 0) mma_commit(bar + 8 * C::bDone);
+  if (warp == 1) {
+    if (lane == 0) {  // every tensor-core operation of this CTA has completed
+      mma_commit(bar + 8 * C::bDone);
+      if (!mbar_wait(bar + 8 * C::bDone, 0)) record_error(p.err, kErrDone);
+    }
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Row statistics (padded to whole tiles), and zeros for the gradient rows of
+// tiles that lie past their sequence's length.
+template <int D>
+__global__ void __launch_bounds__(256) sink_rows_kernel(const Params p) {
+  constexpr int TPR = D / 8;  // threads per row, 8 elements (16 bytes) each
+  pdl_trigger();
+  pdl_wait();
+  const int64_t gt = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+  const int64_t row = gt / TPR;
+  const int part = static_cast<int>(gt % TPR);
+  const int64_t bh = row / p.npad;
+  const int q = static_cast<int>(row - bh * p.npad);
+  const bool in = bh < static_cast<int64_t>(p.batch) * p.heads;
+  float acc = 0.f;
+  bool valid = false;
+  if (in) {
+    const int b = static_cast<int>(bh / p.heads), h = static_cast<int>(bh - static_cast<int64_t>(b) * p.heads);
+    const int L = length_of(p, b);
+    valid = q < L;
+    if (valid) {
+      const int64_t at = (bh * p.n + q) * D + part * 8;
+      const uint4 ov = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.o) + at);
+      const uint4 dv = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dout) + at);
+      const __nv_bfloat162* o2 = reinterpret_cast<const __nv_bfloat162*>(&ov);
+      const __nv_bfloat162* d2 = reinterpret_cast<const __nv_bfloat162*>(&dv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 of = __bfloat1622float2(o2[i]);
+        const float2 df = __bfloat1622float2(d2[i]);
+        acc = fmaf(of.x, df.x, acc);
+        acc = fmaf(of.y, df.y, acc);
+      }
+    } else if (q < p.n && q / kRows * kRows >= L) {
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dq) + (bh * p.n + q) * D)[part] = z;
+      if (h % p.group == 0) {
+        const int64_t kv = static_cast<int64_t>(b) * p.kv_heads + h / p.group;
+        reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dk) + (kv * p.n + q) * D)[part] = z;
+        reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dv) + (kv * p.n + q) * D)[part] = z;
+      }
+    }
+  }
+#pragma unroll
+  for (int off = TPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+  if (in && part == 0) {
+    p.nd[row] = -acc;  // stored negated: the main kernels form dP + (-D)
+    p.nlse2[row] = valid ? -p.lse[bh * p.n + q] * kLog2e : -INFINITY;
+  }
+}
+
+// dV and dK of split key tiles: the parts added in order, rounded once.  Block =
+// 1024 / D rows of 128 (grid x: rows of the listed tiles; y: dV, dK).
+template <int D>
+__global__ void __launch_bounds__(256) sink_join_kernel(const Params p, int tiles) {
+  constexpr int TPR = D / 4, kPer = 256 / TPR;  // threads per row, rows per block
+  pdl_trigger();
+  pdl_wait();
+  const int blocks = kRows / kPer;
+  const int64_t tl = blockIdx.x / blocks;  // (sequence and head, listed tile)
+  const int r = static_cast<int>(blockIdx.x % blocks) * kPer + threadIdx.x / TPR;
+  const int c = 4 * (threadIdx.x % TPR), out = blockIdx.y;
+  const int64_t bh = tl / tiles;
+  // the list has tile 0 when it is split, and the others when they are
+  const int tile = static_cast<int>(tl - bh * tiles) + (p.s0 > 1 ? 0 : 1);
+  const int L = length_of(p, static_cast<int>(bh / p.kv_heads));
+  const int k = tile * kRows + r;
+  if (tile * kRows >= L || k >= p.n) return;  // zeroed with the row statistics
+  const int parts = tile == 0 ? p.s0 : p.s1;
+  const float* src = tile == 0
+                         ? p.part0 + bh * parts * 2 * kRows * D
+                         : p.part1 + (bh * (p.ntiles - 1) + tile - 1) * parts * 2 * kRows * D;
+  src += (static_cast<int64_t>(out) * kRows + r) * D + c;
+  const int64_t all = static_cast<int64_t>(query_chunks(tile, L, p.window, p.sinks)) * p.group;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < parts; ++i) {
+    if (all * i / parts == all * (i + 1) / parts) continue;  // an empty part was not written
+    const float4 v = *reinterpret_cast<const float4*>(src + static_cast<int64_t>(i) * 2 * kRows * D);
+    sum.x += v.x;
+    sum.y += v.y;
+    sum.z += v.z;
+    sum.w += v.w;
+  }
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out == 0 ? p.dv : p.dk) + (bh * p.n + k) * D + c;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
+}
+
+struct Plan {
+  int npad, ntiles, s0, s1;
+  int64_t nd, nlse2, part0, part1, bytes;  // workspace offsets and size
+};
+
+// Cuts key tiles into parts when one exceeds an SM's even share of all chunks
+// (never below 16 chunks a part: a part costs a tile of fp32 written and read).
+Plan make_plan(const SinkArgs& a) {
+  Plan w;
+  w.ntiles = (a.n + kRows - 1) / kRows;
+  w.npad = w.ntiles * kRows;
+  const int64_t group = a.heads / a.kv_heads, bkv = static_cast<int64_t>(a.batch) * a.kv_heads;
+  const int64_t c0 = group * query_chunks(0, a.n, a.window, a.sinks);
+  const int64_t c1 = w.ntiles > 1 ? group * query_chunks(1, a.n, a.window, a.sinks) : 0;
+  // tile t >= 1 has min(per, rest - 2 t) chunks a head: its window's, or to the sequence's end
+  const int64_t per = (static_cast<int64_t>(a.window) + kRows - 1 + kChunk - 1) / kChunk;
+  const int64_t rest = (static_cast<int64_t>(a.n) + kChunk - 1) / kChunk, last = w.ntiles - 1;
+  int64_t m = rest > per ? (rest - per) / 2 : 0;  // tiles 1..m have `per`
+  if (m > last) m = last;
+  const int64_t all =
+      c0 + group * (m * per + (last - m) * rest - (last * (last + 1) - m * (m + 1)));
+  int64_t cap = (all * bkv + 147) / 148;
+  if (cap < 16) cap = 16;
+  const int64_t s0 = (c0 + cap - 1) / cap, s1 = (c1 + cap - 1) / cap;
+  w.s0 = static_cast<int>(s0 < 1 ? 1 : s0);
+  w.s1 = static_cast<int>(s1 < 1 ? 1 : s1);
+  const int64_t rows = static_cast<int64_t>(a.batch) * a.heads * w.npad;
+  const int64_t tile = 2ll * kRows * a.d * 4;
+  w.nd = 0;
+  w.nlse2 = align_up(rows * 4, 256);
+  w.part0 = 2 * w.nlse2;
+  w.part1 = w.part0 + (w.s0 > 1 ? bkv * w.s0 * tile : 0);
+  w.bytes = w.part1 + (w.s1 > 1 ? bkv * (w.ntiles - 1) * w.s1 * tile : 0);
+  return w;
+}
+
+template <int D, bool kDQ>
+cudaError_t launch_main(const SinkArgs& a, Params p, cudaStream_t stream) {
+  using C = Cfg<D, kDQ>;
+  const int64_t hq = static_cast<int64_t>(a.batch) * a.heads;
+  const int64_t hk = static_cast<int64_t>(a.batch) * a.kv_heads;
+  CUtensorMap tx, ty, cx, cy, to0, to1;
+  const bool maps =
+      kDQ ? make_tmap_bf16_rows(&tx, a.q, D, a.n, hq, kRows) &&
+                make_tmap_bf16_rows(&ty, a.dout, D, a.n, hq, kRows) &&
+                make_tmap_bf16_rows(&cx, a.k, D, a.n, hk, kChunk) &&
+                make_tmap_bf16_rows(&cy, a.v, D, a.n, hk, kChunk) &&
+                make_tmap_bf16_rows(&to0, a.dq, D, a.n, hq, kRows) &&
+                make_tmap_bf16_rows(&to1, a.dq, D, a.n, hq, kRows)
+          : make_tmap_bf16_rows(&tx, a.k, D, a.n, hk, kRows) &&
+                make_tmap_bf16_rows(&ty, a.v, D, a.n, hk, kRows) &&
+                make_tmap_bf16_rows(&cx, a.q, D, a.n, hq, kChunk) &&
+                make_tmap_bf16_rows(&cy, a.dout, D, a.n, hq, kChunk) &&
+                make_tmap_bf16_rows(&to0, a.dv, D, a.n, hk, kRows) &&
+                make_tmap_bf16_rows(&to1, a.dk, D, a.n, hk, kRows);
+  if (!maps) return cudaErrorInvalidValue;
+  const int64_t items = kDQ ? hq * p.ntiles
+                            : hk * (p.s0 + static_cast<int64_t>(p.ntiles - 1) * p.s1);
+  if (items > (1ll << 30)) return cudaErrorInvalidValue;
+  p.items = static_cast<int>(items);
+  cudaError_t e = cudaFuncSetAttribute(attn_sink_bwd_kernel<D, kDQ>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int grid = static_cast<int>(items < num_sms() ? items : num_sms());
+  return launch_pdl(attn_sink_bwd_kernel<D, kDQ>, dim3(grid), dim3(kThreads), C::kSmem, stream, tx,
+                    ty, cx, cy, to0, to1, p);
+}
+
+template <int D>
+cudaError_t run(const SinkArgs& a, cudaStream_t stream) {
+  const Plan w = make_plan(a);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  Params p = {};
+  p.o = a.o;
+  p.dout = a.dout;
+  p.lse = a.lse;
+  p.lengths = a.lengths;
+  p.dq = a.dq;
+  p.dk = a.dk;
+  p.dv = a.dv;
+  p.nd = reinterpret_cast<float*>(ws + w.nd);
+  p.nlse2 = reinterpret_cast<float*>(ws + w.nlse2);
+  p.part0 = reinterpret_cast<float*>(ws + w.part0);
+  p.part1 = reinterpret_cast<float*>(ws + w.part1);
+  p.err = a.err;
+  p.batch = a.batch;
+  p.heads = a.heads;
+  p.kv_heads = a.kv_heads;
+  p.group = a.heads / a.kv_heads;
+  p.n = a.n;
+  p.npad = w.npad;
+  p.ntiles = w.ntiles;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.s0 = w.s0;
+  p.s1 = w.s1;
+  p.scale = a.scale;
+  const int64_t rows = static_cast<int64_t>(a.batch) * a.heads * w.npad;
+  const int64_t blocks = (rows * (D / 8) + 255) / 256;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  cudaError_t e = launch_pdl(sink_rows_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                             stream, p);
+  if (e == cudaSuccess) e = launch_main<D, false>(a, p, stream);
+  if (e == cudaSuccess) e = launch_main<D, true>(a, p, stream);
+  if (e != cudaSuccess) return e;
+  const int tiles = (w.s0 > 1 ? 1 : 0) + (w.s1 > 1 ? w.ntiles - 1 : 0);
+  if (tiles == 0) return cudaSuccess;
+  const int64_t joins = static_cast<int64_t>(a.batch) * a.kv_heads * tiles * (kRows / (1024 / D));
+  if (joins > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_pdl(sink_join_kernel<D>, dim3(static_cast<unsigned>(joins), 2), dim3(256), 0, stream,
+                    p, tiles);
+}
+
+}  // namespace
+
+size_t sink_bwd_workspace_bytes(const SinkArgs& a) { return static_cast<size_t>(make_plan(a).bytes); }
+
+cudaError_t launch_attn_sink_bwd(const SinkArgs& a, cudaStream_t stream) {
+  return a.d == 64 ? run<64>(a, stream) : run<128>(a, stream);
+}
+
+}  // namespace nb

@@ -30,6 +30,24 @@ struct AttnArgs {
   bool causal;        // causal band: key blocks i - R..i of query block i, keys k <= q
 };
 
+// Arguments of an attention call with a window and sinks, validated on the host.
+struct SinkArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* o;      // forward: output; backward: input
+  const void* dout;   // backward only
+  float* lse;         // forward: output (may be null); backward: input
+  const int32_t* lengths;  // may be null = all full
+  void* dq;
+  void* dk;
+  void* dv;
+  void* workspace;
+  int* err;
+  int batch, heads, kv_heads, n, d, window, sinks;
+  float scale;        // 1/sqrt(d)
+};
+
 // Arguments of a write to or a read from the 4-bit cache.
 struct Kv4Args {
   void* k;  // write: input; read: output
@@ -128,6 +146,9 @@ cudaError_t launch_tokenize_batch(const uint8_t* seqs, const int64_t* offsets, i
 cudaError_t launch_attn_fwd_f32(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_fwd_bf16_tc(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_bwd_bf16(const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_sink_fwd(const SinkArgs& a, cudaStream_t stream);
+size_t sink_bwd_workspace_bytes(const SinkArgs& a);
+cudaError_t launch_attn_sink_bwd(const SinkArgs& a, cudaStream_t stream);
 int kv4_page_bytes(int d);  // d = 64 or 128
 cudaError_t launch_kv4(const Kv4Args& a, bool write, cudaStream_t stream);
 size_t kv4_decode_workspace_bytes(const Kv4DecodeArgs& a);

@@ -1,7 +1,8 @@
 /*
  * nb.h - C ABI of the B200 (sm_100a) banded block-sparse local attention, the
- * fused 2-bit DNA k-mer tokenizer, and the operators that serve a causal model
- * over long sequences: a 4-bit key/value cache and single-token attention over it.
+ * fused 2-bit DNA k-mer tokenizer, and the operators that train and serve a
+ * causal model over long sequences: attention with a sliding window and visible
+ * first tokens, a 4-bit key/value cache, and single-token attention over it.
  *
  * The operations follow the NucleoByte page ("NucleoByte: GPU-Accelerated
  * Block-Sparse Genomic Language Model"):
@@ -36,7 +37,7 @@
  *     returns NB_ERR_CUDA.  Kernels never trap.
  *   - Attention tensors are [batch, heads, n, d] contiguous with d innermost;
  *     log-sum-exp and the row term are [batch, heads, n] fp32.  n must be a
- *     multiple of 32 (any n for nb_kv4_*) and d is 64 or 128.
+ *     multiple of 32 (any n for nb_attn_sink_* and nb_kv4_*) and d is 64 or 128.
  *     Tensor pointers must be 16-byte aligned.
  *   - `lengths` (optional, int32 [batch], device) gives each sequence's true
  *     length L_b in [0, n]; NULL means every L_b = n.  Keys k >= L_b are
@@ -295,7 +296,49 @@ NB_API nb_status nb_tokenize_batch(const uint8_t* seqs, const int64_t* offsets, 
  */
 NB_API nb_status nb_batch_ceiling(const int64_t* offsets, int batch, int k, int32_t* n_pad);
 
-#define NB_MAX_SINKS 128 /* first tokens that can stay visible */
+/*
+ * nb_attn_sink_fwd - causal attention with a sliding window of `window` tokens
+ * in which the first `sinks` tokens stay visible, forward.  The NucleoByte page
+ * has no counterpart: it is the token-level form of the causal band above, for
+ * sequences much longer than the band.
+ *   Query q sees key k when k <= q, k < L_b and (q - k < window or k < sinks).
+ *   O = softmax over the visible keys of Q K^T / sqrt(d), times V.
+ * q       in : [batch, heads, n, d] of `dtype`.
+ * k, v    in : [batch, kv_heads, n, d]; heads is a multiple of kv_heads, and
+ *              query head h reads key/value head h / (heads / kv_heads).
+ * o, lse  out: as nb_attn_fwd (lse may be NULL).
+ * lengths in : int32 [batch] or NULL (see conventions).  What rows past a
+ *              sequence's length hold, NaN included, does not matter.
+ * n >= 0, any value; window >= 1 (n or more: plain causal attention);
+ * 0 <= sinks <= NB_MAX_SINKS (more returns NB_ERR_UNSUPPORTED).
+ * NB_BF16 only (NB_F32 returns NB_ERR_UNSUPPORTED).
+ */
+#define NB_MAX_SINKS 128
+NB_API nb_status nb_attn_sink_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
+                                  const int32_t* lengths, int batch, int heads, int kv_heads, int n,
+                                  int d, int window, int sinks, int dtype, void* stream);
+
+/*
+ * nb_attn_sink_bwd - backward of nb_attn_sink_fwd from its stored log-sum-exp:
+ * D = rowsum(dO O), dS = P (dO V^T - D), dV = P^T dO, dQ = dS K / sqrt(d),
+ * dK = dS^T Q / sqrt(d); dK and dV are summed over the query heads that share a
+ * key/value head.  All three gradients are deterministic.
+ * q, k, v, o, lse, dout in : as nb_attn_bwd, with k, v of kv_heads heads.
+ * dq         out: [batch, heads, n, d];  dk, dv out: [batch, kv_heads, n, d].
+ *                 Rows past a sequence's length are written as 0.  The outputs
+ *                 must not alias the inputs.
+ * workspace     : device scratch of at least nb_attn_sink_bwd_workspace_size(...)
+ *                 bytes, 256-byte aligned; contents on entry do not matter.  It
+ *                 must not be used by another call that runs concurrently.
+ * Sizes, limits and types as nb_attn_sink_fwd.
+ */
+NB_API size_t nb_attn_sink_bwd_workspace_size(int batch, int heads, int kv_heads, int n, int d,
+                                              int window, int sinks, int dtype);
+NB_API nb_status nb_attn_sink_bwd(const void* q, const void* k, const void* v, const void* o,
+                                  const void* dout, const float* lse, const int32_t* lengths,
+                                  void* dq, void* dk, void* dv, void* workspace,
+                                  size_t workspace_bytes, int batch, int heads, int kv_heads, int n,
+                                  int d, int window, int sinks, int dtype, void* stream);
 
 /*
  * The 4-bit key/value cache.  A pool of pages of NB_KV4_PAGE tokens,
@@ -345,10 +388,10 @@ NB_API nb_status nb_kv4_read(const void* cache, const int32_t* block_table, cons
                              int d, int max_pages, int num_pages, int dtype, void* stream);
 
 /*
- * nb_attn_kv4_decode - attention of the last token of each sequence over keys and
- * values from the 4-bit cache, with a sliding window and visible first tokens
- * (sinks): the query of sequence b has position lengths[b] - 1 and sees token
- * k < lengths[b] when k >= lengths[b] - window or k < sinks.
+ * nb_attn_kv4_decode - nb_attn_sink_fwd for the last token of each sequence, with
+ * keys and values from the 4-bit cache: the query of sequence b has position
+ * lengths[b] - 1 and sees token k < lengths[b] when k >= lengths[b] - window or
+ * k < sinks.
  * q           in : [batch, heads, d] bf16; heads a multiple of kv_heads.
  * cache, block_table in: as nb_kv4_read.  Only pages that hold a visible token
  *                  are read; the others need not be mapped.  A visible token on
