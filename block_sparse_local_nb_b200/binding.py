@@ -82,11 +82,30 @@ def _ptr(x):
     return x.data_ptr()
 
 
-def _stream(stream):
-    if stream is None:
+_raw_stream = None
+
+
+def _current_stream():
+    """Handle of the current stream of the current device.  torch's raw getter takes
+    0.2 us; torch.cuda.current_stream(), used where a torch lacks it, 3.2 us (a
+    third of a small call)."""
+    global _raw_stream
+    if _raw_stream is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        torch.cuda.current_stream()  # initialises CUDA
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        if raw is not None and device is not None:
+            _raw_stream = lambda: raw(device())  # noqa: E731
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _raw_stream()
+
+
+def _stream(stream):
+    if stream is None:
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -204,8 +204,8 @@ nb_status check_decode(int batch, int heads, int kv_heads, int d, int max_pages,
   if (heads < 0 || heads % kv_heads != 0 || window < 1 || sinks < 0) return NB_ERR_INVALID_ARG;
   if (dtype != NB_F32 && dtype != NB_BF16) return NB_ERR_INVALID_ARG;
   if (dtype != NB_BF16 || sinks > NB_MAX_SINKS) return NB_ERR_UNSUPPORTED;
-  // rows of partial results, and blocks, fit 31 bits
-  if (static_cast<double>(batch) * heads * 256 > INT32_MAX) return NB_ERR_UNSUPPORTED;
+  // rows, and blocks (few shares a row when there are many rows), fit 31 bits
+  if (static_cast<double>(batch) * heads > INT32_MAX / 4) return NB_ERR_UNSUPPORTED;
   return NB_OK;
 }
 

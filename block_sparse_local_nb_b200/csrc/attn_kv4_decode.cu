@@ -2,16 +2,20 @@
 // sliding window and visible first tokens (layout of the cache in kv4.cuh).
 //
 // With key value k_j = m_jg + s_jg (c - 7.5) on channel group g,
-//   q . k_j = sum_g s_jg (q_g . c_jg) + (m_jg - 7.5 s_jg) sum(q_g)
+//   q . k_j = sum_g s_jg (q_g . c_jg - 7.5 sum(q_g)) + sum_g m_jg sum(q_g)
 //   O = sum_j p_j v_j = sum_j (p_j s_jg)(c - 7.5) + sum_j p_j m_jg
-// so the codes themselves are the operands of a warp matrix product (m16n8k16,
-// rows = the query heads that share the key/value head): no row is ever
-// dequantised in memory, and s and m enter in fp32 outside the products.  A
-// nibble becomes bf16 by or-ing it into the mantissa of 32 (32 + c, exact); the
-// 39.5 = 32 + 7.5 is taken off through sum(q_g) for the keys and by an exact
-// bf16 subtraction for the values.  Softmax statistics, sums and outputs are
-// fp32; p s is rounded to bf16 as the operand of the value product (the output
-// is bf16, and each p carries an error of its own).
+// so the codes themselves are the operands of warp matrix products (m16n8k16): no
+// row is ever dequantised in memory, and s and m enter in fp32 outside them.  A
+// nibble becomes bf16 by or-ing it into the mantissa of 128 (128 + c, exact).
+//   Scores: rows = 16 tokens, columns = 8 query heads that share the key/value
+//   head; the products start from -135.5 sum(q_g), so 128 + 7.5 is off again in
+//   fp32.  sum_g m_jg sum(q_g) is one product more, over the bf16 midpoints and
+//   sum(q_g) cut into three bf16 parts (24 bits).
+//   Values: rows = 16 channels, columns = 8 heads; here the offset is subtracted
+//   from the codes before the product (exact in bf16), because the output sums
+//   over many tokens and would cancel.  p s is rounded to bf16 and transposed
+//   within the warp to become the operand (the output is bf16 and every token's
+//   error is its own); softmax statistics, sum p m and the outputs are fp32.
 //
 // A block of four warps takes one key/value head of one sequence and a share of
 // its visible pages (the pages of the sinks, then those of the window); warp w
@@ -19,6 +23,8 @@
 // ring, and keeps its own maximum, sum and output.  The warps, and then the
 // shares, are joined by their maxima.  Bound by memory: the page bytes, once.
 #include <math.h>
+
+#include <type_traits>
 
 #include "kv4.cuh"
 #include "nb_internal.h"
@@ -33,6 +39,8 @@ using namespace sm100;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kHeads = 16;  // query heads of one block (the rows of a product)
+constexpr int kMinShare = 4 * kWarps;  // pages: a share of fewer costs more than it gains
+constexpr float kTau = 8.0f;           // lazy-rescale threshold, log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -42,7 +50,9 @@ struct Cfg {
   static constexpr int kStages = 3;
   static constexpr int kRing = kWarps * kStages * P::kBytes;
   // the warps' results take the place of the ring when the pages are done
-  static constexpr int kJoin = kWarps * kHeads * (D + 2) * 4;
+  // (rows of D + 4 floats: the lanes of a store fall into different banks)
+  static constexpr int kJoinRow = D + 4;
+  static constexpr int kJoin = kWarps * kHeads * (kJoinRow + 2 + P::kGroups) * 4;
   static constexpr int oBar = kRing > kJoin ? kRing : kJoin;
   static constexpr int oOk = oBar + kWarps * kStages * 8;  // 1: the stage holds a page
   static constexpr int kSmem = oOk + kWarps * kStages * 4;
@@ -84,27 +94,50 @@ __device__ __forceinline__ Visible visible_pages(const Params& p, int b) {
   return v;
 }
 
+// d = a b + c (a row-major 16 x 16, b 16 x 8, bf16 in, fp32 out).
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
+                                         uint32_t b1, const float (&c)[4]) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      "{%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+        "f"(c[2]), "f"(c[3]));
 }
 
-// Nibbles i and i + 4 of w as the bf16 pair (32 + c_i, 32 + c_{i+4}).
-template <int I>
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
-  const uint32_t x = I == 0 ? w << 2 : w >> (4 * I - 2);
-  return (x & 0x003c003cu) | 0x42004200u;
+// (x & mask) | magic in one instruction: the operands come in registers, since an
+// instruction takes one immediate only.
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(mask), "r"(magic));
+  return r;
 }
-// the same minus 39.5: c - 7.5, exact
+struct Magic {
+  uint32_t kmask, kbase;  // nibbles at bit 0 of both halves; 128 as bf16
+  uint32_t vmask, vbase;  // nibbles at bit 2; 32
+  uint32_t centre;        // 39.5
+};
+// Values that the compiler cannot fold back into immediates.
+__device__ __forceinline__ Magic make_magic() {
+  Magic m;
+  asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(m.kmask));
+  asm volatile("mov.b32 %0, 0x43004300;" : "=r"(m.kbase));
+  asm volatile("mov.b32 %0, 0x003c003c;" : "=r"(m.vmask));
+  asm volatile("mov.b32 %0, 0x42004200;" : "=r"(m.vbase));
+  asm volatile("mov.b32 %0, 0x421e421e;" : "=r"(m.centre));
+  return m;
+}
+
+// Nibbles i and i + 4 of w as the bf16 pair (128 + c_i, 128 + c_{i+4}).
 template <int I>
-__device__ __forceinline__ uint32_t centred_bf16(uint32_t w) {
-  const uint32_t x = codes_bf16<I>(w);
-  const uint32_t c = 0x421e421eu;  // 39.5, 39.5
+__device__ __forceinline__ uint32_t codes_bf16(const Magic& m, uint32_t w) {
+  return and_or(w >> (4 * I), m.kmask, m.kbase);
+}
+// (c_i - 7.5, c_{i+4} - 7.5): 32 + c (the nibble two bits up) minus 39.5, exact
+template <int I>
+__device__ __forceinline__ uint32_t centred_bf16(const Magic& m, uint32_t w) {
+  const uint32_t x = and_or(I == 0 ? w << 2 : w >> (4 * I - 2), m.vmask, m.vbase);
   __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x),
-                             *reinterpret_cast<const __nv_bfloat162*>(&c));
+                             *reinterpret_cast<const __nv_bfloat162*>(&m.centre));
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
@@ -126,10 +159,21 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[N], const uint8_t* p) {
   }
 }
 
-// kRows: 1 when at most eight heads share the cache (rows 8..15 of the products
-// are zero), 2 otherwise.
-template <int D, int kRows>
-__global__ void __launch_bounds__(kThreads) kv4_decode_kernel(const Params p) {
+// The 8 x 8 matrix of 16-bit values held two a lane (row r, columns 2 t, 2 t + 1),
+// transposed.
+__device__ __forceinline__ uint32_t transpose_b16(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Blocks that should fit an SM at once (registers; the shared memory follows).
+constexpr int blocks_per_sm(int d, int sets) { return d == 64 ? (sets == 1 ? 4 : 3) : (sets == 1 ? 3 : 2); }
+
+// kSets: sets of eight heads (the columns of a product): 1 when at most eight
+// share the cache, 2 otherwise.
+template <int D, int kSets>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_kernel(const Params p) {
   using C = Cfg<D>;
   using P = Page<D>;
   constexpr int NG = P::kGroups, NV = D / 64;
@@ -157,8 +201,8 @@ __global__ void __launch_bounds__(kThreads) kv4_decode_kernel(const Params p) {
   const int nh = min(kHeads, p.group - hb * kHeads);
 
   const Visible vis = visible_pages(p, b);
-  const int i0 = static_cast<int>(static_cast<int64_t>(vis.count) * split / p.splits);
-  const int i1 = static_cast<int>(static_cast<int64_t>(vis.count) * (split + 1) / p.splits);
+  const int share = max(kMinShare, (vis.count + p.splits - 1) / p.splits);
+  const int i0 = min(split * share, vis.count), i1 = min(i0 + share, vis.count);
   const int mine = i1 - i0 > warp ? (i1 - i0 - warp + kWarps - 1) / kWarps : 0;  // this warp's pages
   auto page_of = [&](int i) {  // logical page of this warp's i-th page
     const int x = i0 + warp + i * kWarps;
@@ -167,14 +211,13 @@ __global__ void __launch_bounds__(kThreads) kv4_decode_kernel(const Params p) {
   const int32_t* table = p.pool.table + static_cast<int64_t>(b) * p.pool.max_pages;
   int ids = lane < mine ? table[page_of(lane)] : -1;  // 32 table entries, one per lane
   int ids_from = 0;
-  auto issue = [&](int i) {  // all lanes; brings this warp's i-th page
+  auto issue = [&](int i, int st) {  // all lanes; brings this warp's i-th page into stage st
     if (i - ids_from == 32) {
       ids_from = i;
       ids = i + lane < mine ? table[page_of(i + lane)] : -1;
     }
     const int id = __shfl_sync(0xffffffffu, ids, i - ids_from);
     if (lane == 0) {
-      const int st = i % C::kStages;
       const bool good = id >= 0 && id < p.pool.num_pages;
       ok[st] = good;
       if (good) {
@@ -188,224 +231,275 @@ __global__ void __launch_bounds__(kThreads) kv4_decode_kernel(const Params p) {
       }
     }
   };
-  for (int i = 0; i < min(C::kStages, mine); ++i) issue(i);
+  for (int i = 0; i < min(C::kStages, mine); ++i) issue(i, i);
 
-  // query operand: k-step 2 g + s of the products holds channels 32 g + 8 t + 2 s
+  // query operand: k-step 2 g + i of the products holds channels 32 g + 8 t + 2 i
   // + {0, 4} (first half) and {1, 5} (second half) of lane t, matching the nibble
-  // pairs of a code word; qs_g = sum of q over the group
-  uint32_t qa[2 * NG][4];
-  float qs[kRows][NG];
+  // pairs of a code word.  off_g = -135.5 sum(q_g) of heads 2 t, 2 t + 1.
+  constexpr int NP = NG / 2;
+  uint32_t qb[kSets][2 * NG][2], qm[kSets][2];
+  float off[kSets][NG][2];
 #pragma unroll
-  for (int hr = 0; hr < 2; ++hr) {
-    const int head = r + 8 * hr;
-    const bool in = hr < kRows && head < nh;
+  for (int hs = 0; hs < kSets; ++hs) {
+    const int head = r + 8 * hs;
+    const bool in = head < nh;
     const uint4* src = reinterpret_cast<const uint4*>(
         p.q + (static_cast<int64_t>(b) * p.heads + head0 + (in ? head : 0)) * D);
+    float qs[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const uint4 x = in ? src[4 * g + t] : make_uint4(0, 0, 0, 0);  // channels 32 g + 8 t ..+ 7
-      qa[2 * g][hr] = __byte_perm(x.x, x.z, 0x5410);          // 0, 4
-      qa[2 * g][2 + hr] = __byte_perm(x.x, x.z, 0x7632);      // 1, 5
-      qa[2 * g + 1][hr] = __byte_perm(x.y, x.w, 0x5410);      // 2, 6
-      qa[2 * g + 1][2 + hr] = __byte_perm(x.y, x.w, 0x7632);  // 3, 7
-      if (hr < kRows) {
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        float sum = 0.f;
+      qb[hs][2 * g][0] = __byte_perm(x.x, x.z, 0x5410);      // 0, 4
+      qb[hs][2 * g][1] = __byte_perm(x.x, x.z, 0x7632);      // 1, 5
+      qb[hs][2 * g + 1][0] = __byte_perm(x.y, x.w, 0x5410);  // 2, 6
+      qb[hs][2 * g + 1][1] = __byte_perm(x.y, x.w, 0x7632);  // 3, 7
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          sum += __uint_as_float(w[i] << 16) + __uint_as_float(w[i] & 0xffff0000u);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qs[hr < kRows ? hr : 0][g] = sum;
+      for (int i = 0; i < 4; ++i)
+        sum += __uint_as_float(w[i] << 16) + __uint_as_float(w[i] & 0xffff0000u);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      qs[g] = sum;
+      off[hs][g][0] = -135.5f * __shfl_sync(0xffffffffu, sum, 8 * t);
+      off[hs][g][1] = -135.5f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+    }
+    // lane t of the midpoint product multiplies the pair (m_2u, m_2u+1), u = t mod
+    // NP, by part t / NP of the sums (and by one part more in its second half)
+    const int u = t % NP, part = t / NP;
+    float x0 = u == 0 ? qs[0] : qs[NG - 2], x1 = u == 0 ? qs[1] : qs[NG - 1];
+    uint32_t parts[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      parts[i] = pack_bf16(x0, x1);
+      x0 -= __uint_as_float(parts[i] << 16);
+      x1 -= __uint_as_float(parts[i] & 0xffff0000u);
+    }
+    qm[hs][0] = part == 0 ? parts[0] : part == 1 ? parts[1] : part == 2 ? parts[2] : 0u;
+    qm[hs][1] = NP == 2 && part == 0 ? parts[2] : 0u;
+  }
+
+  // of heads 2 t + j (+ 8 hs): the maximum in use, this lane's sums of p and of p m_g
+  // (its tokens are 16 i + r, + 8), and the output at channels 16 i + r, + 8
+  float m[kSets][2], l[kSets][2], om[kSets][2][NG], o[kSets][D / 16][4];
+#pragma unroll
+  for (int hs = 0; hs < kSets; ++hs) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      m[hs][j] = -INFINITY;
+      l[hs][j] = 0.f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) om[hs][j][g] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[hs][i][e] = 0.f;
+  }
+
+  const Magic mg = make_magic();
+  // One page; kWhole: every token of it is visible (all but the edge pages), which
+  // keeps the common path free of branches.
+  auto page = [&](const uint8_t* pg, int tok0, auto whole_tag) {
+    constexpr bool kWhole = decltype(whole_tag)::value;
+    auto seen = [&](int tok) {
+      return tok0 + tok < vis.len && (tok0 + tok >= vis.first || tok0 + tok < p.sinks);
+    };
+    float s[kSets][2][4];  // scores of tokens 16 mt + r (heads 2 t, 2 t + 1) and + 8
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      uint32_t w[2][NG], par[2][NG], mw[2][2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int tok = 16 * mt + 8 * e + r;
+        lds_words(w[e], pg + P::oK + tok * P::kRow + t * (4 * NG));
+        lds_words(par[e], pg + P::oKPar + tok * P::kParRow);
+        lds_words(mw[e], pg + P::oKPar + tok * P::kParRow + (t % NP) * 8);
+      }
+      const uint32_t m0 = __byte_perm(mw[0][0], mw[0][1], 0x7632);
+      const uint32_t m1 = __byte_perm(mw[1][0], mw[1][1], 0x7632);
+      const uint32_t ma[4] = {m0, m1, m0, m1};
+      const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int hs = 0; hs < kSets; ++hs)
+        mma16816(s[hs][mt], ma, qm[hs][0], qm[hs][1], zero);  // sum_g m_g sum(q_g)
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const uint32_t a0[4] = {codes_bf16<0>(mg, w[0][g]), codes_bf16<0>(mg, w[1][g]),
+                                codes_bf16<1>(mg, w[0][g]), codes_bf16<1>(mg, w[1][g])};
+        const uint32_t a1[4] = {codes_bf16<2>(mg, w[0][g]), codes_bf16<2>(mg, w[1][g]),
+                                codes_bf16<3>(mg, w[0][g]), codes_bf16<3>(mg, w[1][g])};
+        const float st0 = step_of(par[0][g]), st1 = step_of(par[1][g]);
+#pragma unroll
+        for (int hs = 0; hs < kSets; ++hs) {
+          float acc[4] = {off[hs][g][0], off[hs][g][1], off[hs][g][0], off[hs][g][1]};
+          mma16816(acc, a0, qb[hs][2 * g][0], qb[hs][2 * g][1], acc);
+          mma16816(acc, a1, qb[hs][2 * g + 1][0], qb[hs][2 * g + 1][1], acc);
+          s[hs][mt][0] = fmaf(st0, acc[0], s[hs][mt][0]);
+          s[hs][mt][1] = fmaf(st0, acc[1], s[hs][mt][1]);
+          s[hs][mt][2] = fmaf(st1, acc[2], s[hs][mt][2]);
+          s[hs][mt][3] = fmaf(st1, acc[3], s[hs][mt][3]);
+        }
+      }
+      if (!kWhole) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bool v = seen(16 * mt + 8 * e + r);
+#pragma unroll
+          for (int hs = 0; hs < kSets; ++hs)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              s[hs][mt][2 * e + j] = v ? s[hs][mt][2 * e + j] : -INFINITY;
+        }
       }
     }
-  }
-
-  float m[kRows], l[kRows], om[kRows][NG];  // running max, this lane's sum and sum of p m_g
-  float o[D / 8][2 * kRows];                // output: channels 8 i + 2 t, + 1 of heads r (, r + 8)
 #pragma unroll
-  for (int hr = 0; hr < kRows; ++hr) {
-    m[hr] = -INFINITY;
-    l[hr] = 0.f;
+    for (int hs = 0; hs < kSets; ++hs) {
+      float mx[2];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) om[hr][g] = 0.f;
-  }
+      for (int j = 0; j < 2; ++j) {
+        mx[j] = fmaxf(fmaxf(s[hs][0][j], s[hs][0][2 + j]), fmaxf(s[hs][1][j], s[hs][1][2 + j]));
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i)
+        for (int x = 4; x < 32; x <<= 1)
+          mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], x));
+        mx[j] *= p.sl2;
+      }
+      // the maximum in use may lag by 2^8: exact after the final division
+      if (__any_sync(0xffffffffu, mx[0] > m[hs][0] + kTau || mx[1] > m[hs][1] + kTau)) {
 #pragma unroll
-    for (int e = 0; e < 2 * kRows; ++e) o[i][e] = 0.f;
+        for (int j = 0; j < 2; ++j) {
+          const float mn = fmaxf(m[hs][j], mx[j]);
+          const float a = m[hs][j] == -INFINITY ? 0.f : ex2_approx(m[hs][j] - mn);
+          m[hs][j] = mn;
+          l[hs][j] *= a;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) om[hs][j][g] *= a;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            o[hs][c][j] *= a;
+            o[hs][c][2 + j] *= a;
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float nm = m[hs][j] == -INFINITY ? 0.f : -m[hs][j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float& x = s[hs][i >> 1][2 * (i & 1) + j];
+          x = ex2_approx(fmaf(x, p.sl2, nm));
+          l[hs][j] += x;
+        }
+      }
+    }
+    // values: 16 tokens at a time
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      uint32_t ps[kSets][NG][2], vw[4][NV];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int tok = 16 * kk + 8 * e + r;
+        uint32_t par[NG];
+        lds_words(par, pg + P::oVPar + tok * P::kParRow);
+        if (!kWhole && !seen(tok)) {  // unseen tokens may hold anything, NaN too
+#pragma unroll
+          for (int g = 0; g < NG; ++g) par[g] = 0u;
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float step = step_of(par[g]), mid = mid_of(par[g]);
+#pragma unroll
+          for (int hs = 0; hs < kSets; ++hs) {
+            const float p0 = s[hs][kk][2 * e], p1 = s[hs][kk][2 * e + 1];
+            ps[hs][g][e] = transpose_b16(pack_bf16(p0 * step, p1 * step));
+            om[hs][0][g] = fmaf(p0, mid, om[hs][0][g]);
+            om[hs][1][g] = fmaf(p1, mid, om[hs][1][g]);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // the operand's tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+        const int tok = 16 * kk + 2 * t + (e & 1) + 8 * (e >> 1);
+        lds_words(vw[e], pg + P::oV + tok * P::kRow + P::v_chunk(tok, r));
+      }
+#pragma unroll
+      for (int w = 0; w < NV; ++w) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // nibbles 0-3, 4-7: channel groups 2 w, 2 w + 1
+          const uint32_t sel = half ? 0x7632u : 0x5410u;
+          const uint32_t x = __byte_perm(vw[0][w], vw[1][w], sel);
+          const uint32_t y = __byte_perm(vw[2][w], vw[3][w], sel);
+          const uint32_t a0[4] = {centred_bf16<0>(mg, x), centred_bf16<1>(mg, x),
+                                  centred_bf16<0>(mg, y), centred_bf16<1>(mg, y)};
+          const uint32_t a1[4] = {centred_bf16<2>(mg, x), centred_bf16<3>(mg, x),
+                                  centred_bf16<2>(mg, y), centred_bf16<3>(mg, y)};
+          const int g = 2 * w + half;
+#pragma unroll
+          for (int hs = 0; hs < kSets; ++hs) {
+            mma16816(o[hs][2 * g], a0, ps[hs][g][0], ps[hs][g][1], o[hs][2 * g]);
+            mma16816(o[hs][2 * g + 1], a1, ps[hs][g][0], ps[hs][g][1], o[hs][2 * g + 1]);
+          }
+        }
+      }
+    }
+  };
 
   bool timed_out = false;
+  int st = 0, phase = 0;
   for (int i = 0; i < mine; ++i) {
-    const int st = i % C::kStages;
-    if (!__all_sync(0xffffffffu, mbar_wait(bar + 8 * st, (i / C::kStages) & 1))) {
+    if (!__all_sync(0xffffffffu, mbar_wait(bar + 8 * st, phase))) {
       if (lane == 0) record_error(p.err, kErrDecodeWait);
       timed_out = true;
       break;
     }
     if (ok[st]) {
-      const uint8_t* pg = ring + st * P::kBytes;
       const int tok0 = page_of(i) * kPage;
-      // every token of the page is visible (the rule for all but the edge pages)
-      const bool whole = tok0 + kPage <= vis.len && (tok0 >= vis.first || tok0 + kPage <= p.sinks);
-      auto seen = [&](int tok) { return tok < vis.len && (tok >= vis.first || tok < p.sinks); };
-
-      // scores of tokens 8 nt + 2 t, + 1
-      float s[kRows][4][2];
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        uint32_t w[NG];
-        lds_words(w, pg + P::oK + (8 * nt + r) * P::kRow + t * (4 * NG));
-        uint32_t par[2][NG];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          lds_words(par[e], pg + P::oKPar + (8 * nt + 2 * t + e) * P::kParRow);
-#pragma unroll
-        for (int hr = 0; hr < kRows; ++hr) s[hr][nt][0] = s[hr][nt][1] = 0.f;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816(acc, qa[2 * g], codes_bf16<0>(w[g]), codes_bf16<1>(w[g]));
-          mma16816(acc, qa[2 * g + 1], codes_bf16<2>(w[g]), codes_bf16<3>(w[g]));
-#pragma unroll
-          for (int hr = 0; hr < kRows; ++hr)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              // s (acc - 39.5 qs) + m qs
-              const float x = fmaf(-39.5f, qs[hr][g], acc[2 * hr + e]);
-              s[hr][nt][e] = fmaf(step_of(par[e][g]), x, s[hr][nt][e]);
-              s[hr][nt][e] = fmaf(mid_of(par[e][g]), qs[hr][g], s[hr][nt][e]);
-            }
-        }
-        if (!whole) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (!seen(tok0 + 8 * nt + 2 * t + e)) {
-#pragma unroll
-              for (int hr = 0; hr < kRows; ++hr) s[hr][nt][e] = -INFINITY;
-            }
-        }
-      }
-#pragma unroll
-      for (int hr = 0; hr < kRows; ++hr) {
-        float mx = fmaxf(fmaxf(fmaxf(s[hr][0][0], s[hr][0][1]), fmaxf(s[hr][1][0], s[hr][1][1])),
-                         fmaxf(fmaxf(s[hr][2][0], s[hr][2][1]), fmaxf(s[hr][3][0], s[hr][3][1])));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        mx *= p.sl2;
-        if (__any_sync(0xffffffffu, mx > m[hr])) {
-          const float mn = fmaxf(m[hr], mx);
-          const float a = m[hr] == -INFINITY ? 0.f : ex2_approx(m[hr] - mn);
-          m[hr] = mn;
-          l[hr] *= a;
-#pragma unroll
-          for (int g = 0; g < NG; ++g) om[hr][g] *= a;
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            o[c][2 * hr] *= a;
-            o[c][2 * hr + 1] *= a;
-          }
-        }
-        const float nm = m[hr] == -INFINITY ? 0.f : -m[hr];
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            s[hr][nt][e] = ex2_approx(fmaf(s[hr][nt][e], p.sl2, nm));
-            l[hr] += s[hr][nt][e];
-          }
-      }
-      // values: 16 tokens 16 kk + {2 t, 2 t + 1, 2 t + 8, 2 t + 9} at a time
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        uint32_t a[NG][4], vw[4][NV];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int tok = 16 * kk + 2 * t + (e & 1) + 8 * (e >> 1);
-          lds_words(vw[e], pg + P::oV + tok * P::kRow + P::v_chunk(tok, r));
-        }
-#pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {  // the two tokens of each operand half
-          uint32_t par[2][NG];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int tok = 16 * kk + 2 * t + e + 8 * h2;
-            lds_words(par[e], pg + P::oVPar + tok * P::kParRow);
-            if (!whole && !seen(tok0 + tok)) {  // unseen tokens may hold anything, NaN too
-#pragma unroll
-              for (int g = 0; g < NG; ++g) par[e][g] = 0u;
-            }
-          }
-#pragma unroll
-          for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int hr = 0; hr < 2; ++hr) {
-              if (hr < kRows) {
-                const float p0 = s[hr < kRows ? hr : 0][2 * kk + h2][0];
-                const float p1 = s[hr < kRows ? hr : 0][2 * kk + h2][1];
-                a[g][2 * h2 + hr] = pack_bf16(p0 * step_of(par[0][g]), p1 * step_of(par[1][g]));
-                float& acc = om[hr < kRows ? hr : 0][g];
-                acc = fmaf(p0, mid_of(par[0][g]), acc);
-                acc = fmaf(p1, mid_of(par[1][g]), acc);
-              } else {
-                a[g][2 * h2 + hr] = 0u;
-              }
-            }
-        }
-#pragma unroll
-        for (int w = 0; w < NV; ++w) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {  // nibbles 0-3, 4-7: channel groups 2 w, 2 w + 1
-            const uint32_t sel = half ? 0x7632u : 0x5410u;
-            const uint32_t x = __byte_perm(vw[0][w], vw[1][w], sel);
-            const uint32_t y = __byte_perm(vw[2][w], vw[3][w], sel);
-            const uint32_t b0[4] = {centred_bf16<0>(x), centred_bf16<1>(x), centred_bf16<2>(x),
-                                    centred_bf16<3>(x)};
-            const uint32_t b1[4] = {centred_bf16<0>(y), centred_bf16<1>(y), centred_bf16<2>(y),
-                                    centred_bf16<3>(y)};
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const int c = 8 * w + 4 * half + n;
-              float d[4] = {o[c][0], o[c][1], kRows == 2 ? o[c][kRows == 2 ? 2 : 0] : 0.f,
-                            kRows == 2 ? o[c][kRows == 2 ? 3 : 0] : 0.f};
-              mma16816(d, a[2 * w + half], b0[n], b1[n]);
-#pragma unroll
-              for (int e = 0; e < 2 * kRows; ++e) o[c][e] = d[e];
-            }
-          }
-        }
-      }
+      const uint8_t* pg = ring + st * P::kBytes;
+      if (tok0 + kPage <= vis.len && (tok0 >= vis.first || tok0 + kPage <= p.sinks))
+        page(pg, tok0, std::true_type{});
+      else
+        page(pg, tok0, std::false_type{});
     }
     __syncwarp();  // every lane has read the stage: it may be refilled
-    if (i + C::kStages < mine) issue(i + C::kStages);
+    if (i + C::kStages < mine) issue(i + C::kStages, st);
+    if (++st == C::kStages) {
+      st = 0;
+      phase ^= 1;
+    }
   }
   if (timed_out) {  // copies still in flight must land before the block may exit
     for (int i = 0; i < C::kStages; ++i) mbar_wait(bar + 8 * i, 0);
   }
 
-  // the lanes t of a head hold different tokens' sums
-#pragma unroll
-  for (int hr = 0; hr < kRows; ++hr) {
-    l[hr] += __shfl_xor_sync(0xffffffffu, l[hr], 1);
-    l[hr] += __shfl_xor_sync(0xffffffffu, l[hr], 2);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      om[hr][g] += __shfl_xor_sync(0xffffffffu, om[hr][g], 1);
-      om[hr][g] += __shfl_xor_sync(0xffffffffu, om[hr][g], 2);
-    }
-  }
   __syncthreads();  // every warp is done with its ring
-  float* join = reinterpret_cast<float*>(smem);  // [warp][head][d], then [warp][head] (m, l)
-  float2* join_ml = reinterpret_cast<float2*>(join + kWarps * kHeads * D);
+  float* join = reinterpret_cast<float*>(smem);  // [warp][head][d], then (m, l), then sum p m_g
+  float2* join_ml = reinterpret_cast<float2*>(join + kWarps * kHeads * C::kJoinRow);
+  float* join_om = reinterpret_cast<float*>(join_ml + kWarps * kHeads);
 #pragma unroll
-  for (int hr = 0; hr < kRows; ++hr) {
-    const int head = r + 8 * hr;
-    float* dst = join + (warp * kHeads + head) * D;
+  for (int hs = 0; hs < kSets; ++hs) {
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c)
-      *reinterpret_cast<float2*>(dst + 8 * c + 2 * t) =
-          make_float2(o[c][2 * hr] + om[hr][c / 4], o[c][2 * hr + 1] + om[hr][c / 4]);
-    if (t == 0) join_ml[warp * kHeads + head] = make_float2(m[hr], l[hr]);
+    for (int j = 0; j < 2; ++j) {
+      const int at = warp * kHeads + 8 * hs + 2 * t + j;
+      // the lanes r of a head hold different tokens' sums
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        l[hs][j] += __shfl_xor_sync(0xffffffffu, l[hs][j], x);
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          om[hs][j][g] += __shfl_xor_sync(0xffffffffu, om[hs][j][g], x);
+      }
+      if (r == 0) {
+        join_ml[at] = make_float2(m[hs][j], l[hs][j]);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) join_om[at * NG + g] = om[hs][j][g];
+      }
+      float* dst = join + at * C::kJoinRow + r;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        dst[16 * c] = o[hs][c][j];
+        dst[16 * c + 8] = o[hs][c][2 + j];
+      }
+    }
   }
   __syncthreads();
   for (int idx = threadIdx.x; idx < nh * (D / 2); idx += kThreads) {
@@ -417,13 +511,15 @@ __global__ void __launch_bounds__(kThreads) kv4_decode_kernel(const Params p) {
     float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float2 ml = join_ml[w * kHeads + head];
+      const int at = w * kHeads + head;
+      const float2 ml = join_ml[at];
       if (ml.x == -INFINITY) continue;  // this warp saw no token
       const float f = ex2_approx(ml.x - mx);
-      const float2 x = *reinterpret_cast<const float2*>(join + (w * kHeads + head) * D + 2 * c);
+      const float2 x = *reinterpret_cast<const float2*>(join + at * C::kJoinRow + 2 * c);
+      const float mid = join_om[at * NG + c / 16];
       sum = fmaf(ml.y, f, sum);
-      acc.x = fmaf(x.x, f, acc.x);
-      acc.y = fmaf(x.y, f, acc.y);
+      acc.x = fmaf(x.x + mid, f, acc.x);
+      acc.y = fmaf(x.y + mid, f, acc.y);
     }
     const int64_t row = static_cast<int64_t>(b) * p.heads + head0 + head;
     if (p.splits > 1) {
@@ -439,42 +535,60 @@ __global__ void __launch_bounds__(kThreads) kv4_decode_kernel(const Params p) {
   }
 }
 
-// Joins the shares of a row: one warp per (sequence, head).
+// Joins the shares of a row: one block per (sequence, head); warp w takes every
+// eighth share, the warps join through shared memory in order.
+constexpr int kJoinWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(128) kv4_join_kernel(const Params p, int rows) {
+__global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(const Params p) {
+  __shared__ float2 acc_s[kJoinWarps][D / 2];
+  __shared__ float sum_s[kJoinWarps], max_s[kJoinWarps];
   pdl_trigger();
   pdl_wait();
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= rows) return;
+  const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float2* ml = p.part_ml + static_cast<int64_t>(row) * p.splits;
   const float* part = p.part + static_cast<int64_t>(row) * p.splits * D;
   float mx = -INFINITY;
-  for (int s = lane; s < p.splits; s += 32) mx = fmaxf(mx, ml[s].x);
+  for (int s = threadIdx.x; s < p.splits; s += 32 * kJoinWarps) mx = fmaxf(mx, ml[s].x);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-  float sum = 0.f, acc[D / 32];
+  for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+  if (lane == 0) max_s[warp] = mx;
+  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
+  for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, max_s[w]);
+  const bool has = mx != -INFINITY;  // some share saw a token
+  float sum = 0.f;
+  float2 acc[D / 64];
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) acc[i] = make_float2(0.f, 0.f);
+#pragma unroll 4
+  for (int s = warp; s < p.splits; s += kJoinWarps) {
     const float2 x = ml[s];
-    if (x.x == -INFINITY) continue;
+    if (x.x == -INFINITY) continue;  // a share without a visible token
     const float f = ex2_approx(x.x - mx);
     sum = fmaf(x.y, f, sum);
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
       const float2 v = *reinterpret_cast<const float2*>(part + static_cast<int64_t>(s) * D +
                                                         64 * i + 2 * lane);
-      acc[2 * i] = fmaf(v.x, f, acc[2 * i]);
-      acc[2 * i + 1] = fmaf(v.y, f, acc[2 * i + 1]);
+      acc[i] = __ffma2_rn(v, make_float2(f, f), acc[i]);
     }
   }
-  const bool has = mx != -INFINITY;
-  const float inv = has ? 1.f / sum : 0.f;
+  if (lane == 0) sum_s[warp] = sum;
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i)
-    *reinterpret_cast<uint32_t*>(p.o + static_cast<int64_t>(row) * D + 64 * i + 2 * lane) =
-        has ? pack_bf16(acc[2 * i] * inv, acc[2 * i + 1] * inv) : 0u;
-  if (lane == 0 && p.lse) p.lse[row] = has ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+  for (int i = 0; i < D / 64; ++i) acc_s[warp][32 * i + lane] = acc[i];
+  __syncthreads();
+  if (threadIdx.x >= D / 2) return;
+  float2 out = make_float2(0.f, 0.f);
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    out = __fadd2_rn(out, acc_s[w][threadIdx.x]);
+    sum += sum_s[w];
+  }
+  const float inv = has ? 1.f / sum : 0.f;
+  *reinterpret_cast<uint32_t*>(p.o + static_cast<int64_t>(row) * D + 2 * threadIdx.x) =
+      has ? pack_bf16(out.x * inv, out.y * inv) : 0u;
+  if (threadIdx.x == 0 && p.lse) p.lse[row] = has ? (mx + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -485,23 +599,23 @@ int64_t most_pages(const Kv4DecodeArgs& a) {
   return w + s < a.max_pages ? w + s : a.max_pages;
 }
 
-// Shares per sequence and head: enough blocks to fill the GPU, each with a few
-// pages for every warp.
+// Shares per sequence and head: three times the blocks that fit the GPU at once,
+// so that sequences of unequal length even out, and no share below kMinShare pages.
 int splits_for(const Kv4DecodeArgs& a) {
   const int64_t blocks =
       static_cast<int64_t>(a.batch) * a.kv_heads * ceil_div(a.heads / a.kv_heads, kHeads);
-  const int64_t want = ceil_div(148 * 6, blocks);
-  const int64_t most = ceil_div(most_pages(a), 4 * kWarps);
+  const int64_t want = ceil_div(148 * 4 * 3, blocks);
+  const int64_t most = ceil_div(most_pages(a), kMinShare);
   const int64_t s = want < most ? want : most;
-  return static_cast<int>(s < 1 ? 1 : (s > 256 ? 256 : s));
+  return static_cast<int>(s < 1 ? 1 : s);
 }
 
-template <int D, int kRows>
+template <int D, int kSets>
 cudaError_t launch_main(const Params& p, dim3 grid, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<D, kRows>,
+  cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<D, kSets>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv4_decode_kernel<D, kRows>, grid, dim3(kThreads), Cfg<D>::kSmem, stream, p);
+  return launch_pdl(kv4_decode_kernel<D, kSets>, grid, dim3(kThreads), Cfg<D>::kSmem, stream, p);
 }
 
 template <int D>
@@ -530,8 +644,8 @@ cudaError_t run(const Kv4DecodeArgs& a, cudaStream_t stream) {
   cudaError_t e = p.group <= 8 ? launch_main<D, 1>(p, grid, stream)
                                : launch_main<D, 2>(p, grid, stream);
   if (e != cudaSuccess || p.splits == 1) return e;
-  return launch_pdl(kv4_join_kernel<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0,
-                    stream, p, static_cast<int>(rows));
+  return launch_pdl(kv4_join_kernel<D>, dim3(static_cast<unsigned>(rows)), dim3(32 * kJoinWarps), 0,
+                    stream, p);
 }
 
 }  // namespace
