@@ -52,7 +52,7 @@ struct Cfg {
   // the warps' results take the place of the ring when the pages are done
   // (rows of D + 4 floats: the lanes of a store fall into different banks)
   static constexpr int kJoinRow = D + 4;
-  static constexpr int kJoin = kWarps * kHeads * (kJoinRow + 2 + P::kGroups) * 4;
+  static constexpr int kJoin = kHeads * (kWarps * (kJoinRow + 2 + P::kGroups) + 2) * 4;
   static constexpr int oBar = kRing > kJoin ? kRing : kJoin;
   static constexpr int oOk = oBar + kWarps * kStages * 8;  // 1: the stage holds a page
   static constexpr int kSmem = oOk + kWarps * kStages * 4;
@@ -69,6 +69,7 @@ struct Params {
   float2* part_ml;
   int* err;
   int heads, group, head_blocks, splits, window, sinks;
+  bool cluster;  // the shares of a row are one cluster
   float sl2;  // log2(e) / sqrt(d)
 };
 
@@ -165,6 +166,35 @@ __device__ __forceinline__ uint32_t transpose_b16(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+
+constexpr int kMaxCluster = 8;  // blocks of a cluster on every device
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// Two floats at this block's shared-memory address `at`, in block `rank` of the cluster.
+__device__ __forceinline__ float2 load_cluster(uint32_t at, int rank) {
+  float2 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %2, %3;\n\t"
+      "ld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y)
+      : "r"(at), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// Channels 2 c, 2 c + 1 of a finished row; an empty sequence gives 0 and -inf.
+__device__ __forceinline__ void store_row(const Params& p, int d, int64_t row, int c, float2 acc,
+                                          float mx, float sum) {
+  const bool has = mx != -INFINITY;
+  const float inv = has ? 1.f / sum : 0.f;
+  *reinterpret_cast<uint32_t*>(p.o + row * d + 2 * c) =
+      has ? pack_bf16(acc.x * inv, acc.y * inv) : 0u;
+  if (c == 0 && p.lse) p.lse[row] = has ? (mx + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // Blocks that should fit an SM at once (registers; the shared memory follows).
@@ -474,7 +504,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
   __syncthreads();  // every warp is done with its ring
   float* join = reinterpret_cast<float*>(smem);  // [warp][head][d], then (m, l), then sum p m_g
   float2* join_ml = reinterpret_cast<float2*>(join + kWarps * kHeads * C::kJoinRow);
-  float* join_om = reinterpret_cast<float*>(join_ml + kWarps * kHeads);
+  float2* share_ml = join_ml + kWarps * kHeads;  // [head] (m, l) of the whole block
+  float* join_om = reinterpret_cast<float*>(share_ml + kHeads);
 #pragma unroll
   for (int hs = 0; hs < kSets; ++hs) {
 #pragma unroll
@@ -521,32 +552,65 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
       acc.x = fmaf(x.x + mid, f, acc.x);
       acc.y = fmaf(x.y + mid, f, acc.y);
     }
-    const int64_t row = static_cast<int64_t>(b) * p.heads + head0 + head;
-    if (p.splits > 1) {
-      *reinterpret_cast<float2*>(p.part + (row * p.splits + split) * D + 2 * c) = acc;
-      if (c == 0) p.part_ml[row * p.splits + split] = make_float2(mx, sum);
+    if (p.splits == 1) {
+      store_row(p, D, static_cast<int64_t>(b) * p.heads + head0 + head, c, acc, mx, sum);
+    } else if (p.cluster) {  // this thread alone read the place it writes
+      *reinterpret_cast<float2*>(join + head * C::kJoinRow + 2 * c) = acc;
+      if (c == 0) share_ml[head] = make_float2(mx, sum);
     } else {
-      const bool has = mx != -INFINITY;  // an empty sequence: 0 and -inf
-      const float inv = has ? 1.f / sum : 0.f;
-      *reinterpret_cast<uint32_t*>(p.o + row * D + 2 * c) =
-          has ? pack_bf16(acc.x * inv, acc.y * inv) : 0u;
-      if (c == 0 && p.lse) p.lse[row] = has ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+      const int64_t at = (static_cast<int64_t>(b) * p.heads + head0 + head) * p.splits + split;
+      *reinterpret_cast<float2*>(p.part + at * D + 2 * c) = acc;
+      if (c == 0) p.part_ml[at] = make_float2(mx, sum);
     }
   }
+  if (!p.cluster) return;
+  // the blocks of the cluster hold the shares of the same rows: each joins a part of
+  // the output from all blocks' shared memory
+  cluster_sync();
+  for (int idx = split * kThreads + threadIdx.x; idx < nh * (D / 2);
+       idx += p.splits * kThreads) {
+    const int head = idx / (D / 2), c = idx % (D / 2);
+    const uint32_t at_ml = smem_u32(share_ml + head);
+    const uint32_t at = smem_u32(join + head * C::kJoinRow + 2 * c);
+    float2 ml[kMaxCluster], x[kMaxCluster];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kMaxCluster; ++i)
+      if (i < p.splits) {
+        ml[i] = load_cluster(at_ml, i);
+        x[i] = load_cluster(at, i);
+        mx = fmaxf(mx, ml[i].x);
+      }
+    float sum = 0.f;
+    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kMaxCluster; ++i)
+      if (i < p.splits && ml[i].x != -INFINITY) {
+        const float f = ex2_approx(ml[i].x - mx);
+        sum = fmaf(ml[i].y, f, sum);
+        acc.x = fmaf(x[i].x, f, acc.x);
+        acc.y = fmaf(x[i].y, f, acc.y);
+      }
+    store_row(p, D, static_cast<int64_t>(b) * p.heads + head0 + head, c, acc, mx, sum);
+  }
+  cluster_sync();  // no block leaves while another reads its shared memory
 }
 
-// Joins the shares of a row: one block per (sequence, head); warp w takes every
-// eighth share, the warps join through shared memory in order.
-constexpr int kJoinWarps = 8;
-template <int D>
+// Joins the shares of a row: one block per (sequence, head), a share to each
+// D / 4 threads at a time, then the threads' sums in order.
+template <int D, int kJoinWarps>
 __global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(const Params p) {
-  __shared__ float2 acc_s[kJoinWarps][D / 2];
-  __shared__ float sum_s[kJoinWarps], max_s[kJoinWarps];
+  constexpr int kPer = 32 / (D / 4);  // shares that a warp reads at once, 16 bytes a lane
+  constexpr int kAll = kJoinWarps * kPer;
+  __shared__ float4 acc_s[kAll][D / 4];
+  __shared__ float sum_s[kAll], max_s[kJoinWarps];
   pdl_trigger();
   pdl_wait();
   const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = threadIdx.x / (D / 4), c = threadIdx.x % (D / 4);
   const float2* ml = p.part_ml + static_cast<int64_t>(row) * p.splits;
-  const float* part = p.part + static_cast<int64_t>(row) * p.splits * D;
+  const float4* part =
+      reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(row) * p.splits * D) + c;
   float mx = -INFINITY;
   for (int s = threadIdx.x; s < p.splits; s += 32 * kJoinWarps) mx = fmaxf(mx, ml[s].x);
 #pragma unroll
@@ -557,38 +621,36 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(const Params 
   for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, max_s[w]);
   const bool has = mx != -INFINITY;  // some share saw a token
   float sum = 0.f;
-  float2 acc[D / 64];
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) acc[i] = make_float2(0.f, 0.f);
-#pragma unroll 4
-  for (int s = warp; s < p.splits; s += kJoinWarps) {
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int s = sub; s < p.splits; s += kAll) {
     const float2 x = ml[s];
-    if (x.x == -INFINITY) continue;  // a share without a visible token
-    const float f = ex2_approx(x.x - mx);
+    const float4 v = part[static_cast<int64_t>(s) * (D / 4)];
+    const float f = x.x == -INFINITY ? 0.f : ex2_approx(x.x - mx);  // 0: a share without a token
     sum = fmaf(x.y, f, sum);
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const float2 v = *reinterpret_cast<const float2*>(part + static_cast<int64_t>(s) * D +
-                                                        64 * i + 2 * lane);
-      acc[i] = __ffma2_rn(v, make_float2(f, f), acc[i]);
-    }
+    acc.x = fmaf(v.x, f, acc.x);
+    acc.y = fmaf(v.y, f, acc.y);
+    acc.z = fmaf(v.z, f, acc.z);
+    acc.w = fmaf(v.w, f, acc.w);
   }
-  if (lane == 0) sum_s[warp] = sum;
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) acc_s[warp][32 * i + lane] = acc[i];
+  acc_s[sub][c] = acc;
+  if (c == 0) sum_s[sub] = sum;
   __syncthreads();
-  if (threadIdx.x >= D / 2) return;
-  float2 out = make_float2(0.f, 0.f);
-  sum = 0.f;
+  if (sub > 0) return;
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    out = __fadd2_rn(out, acc_s[w][threadIdx.x]);
+  for (int w = 1; w < kAll; ++w) {
+    const float4 v = acc_s[w][c];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
     sum += sum_s[w];
   }
   const float inv = has ? 1.f / sum : 0.f;
-  *reinterpret_cast<uint32_t*>(p.o + static_cast<int64_t>(row) * D + 2 * threadIdx.x) =
-      has ? pack_bf16(out.x * inv, out.y * inv) : 0u;
-  if (threadIdx.x == 0 && p.lse) p.lse[row] = has ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+  *reinterpret_cast<uint2*>(p.o + static_cast<int64_t>(row) * D + 4 * c) =
+      has ? make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv))
+          : make_uint2(0u, 0u);
+  if (c == 0 && p.lse) p.lse[row] = has ? (mx + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -599,23 +661,33 @@ int64_t most_pages(const Kv4DecodeArgs& a) {
   return w + s < a.max_pages ? w + s : a.max_pages;
 }
 
-// Shares per sequence and head: three times the blocks that fit the GPU at once,
-// so that sequences of unequal length even out, and no share below kMinShare pages.
-int splits_for(const Kv4DecodeArgs& a) {
+// Shares per sequence and head: enough blocks to fill the GPU once, and
+// no share below kMinShare pages.  Up
+// to eight shares are one cluster and join through its shared memory; more (a few
+// long sequences) go through the workspace and a second launch.
+struct Plan {
+  int splits;
+  bool cluster;
+};
+Plan plan_for(const Kv4DecodeArgs& a) {
   const int64_t blocks =
       static_cast<int64_t>(a.batch) * a.kv_heads * ceil_div(a.heads / a.kv_heads, kHeads);
-  const int64_t want = ceil_div(148 * 4 * 3, blocks);
+  const int64_t want = ceil_div(148 * 3, blocks);
   const int64_t most = ceil_div(most_pages(a), kMinShare);
-  const int64_t s = want < most ? want : most;
-  return static_cast<int>(s < 1 ? 1 : s);
+  int64_t s = want < most ? want : most;
+  if (s < 1) s = 1;
+  if (s > kMaxCluster && s < 2 * kMaxCluster) s = kMaxCluster;
+  return Plan{static_cast<int>(s), s > 1 && s <= kMaxCluster};
 }
 
 template <int D, int kSets>
 cudaError_t launch_main(const Params& p, dim3 grid, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<D, kSets>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+  auto kernel = kv4_decode_kernel<D, kSets>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv4_decode_kernel<D, kSets>, grid, dim3(kThreads), Cfg<D>::kSmem, stream, p);
+  return launch_pdl_cluster(kernel, grid, dim3(kThreads), Cfg<D>::kSmem, stream,
+                            p.cluster ? p.splits : 1, p);
 }
 
 template <int D>
@@ -631,7 +703,9 @@ cudaError_t run(const Kv4DecodeArgs& a, cudaStream_t stream) {
   p.heads = a.heads;
   p.group = a.heads / a.kv_heads;
   p.head_blocks = (p.group + kHeads - 1) / kHeads;
-  p.splits = splits_for(a);
+  const Plan plan = plan_for(a);
+  p.splits = plan.splits;
+  p.cluster = plan.cluster;
   p.window = a.window;
   p.sinks = a.sinks;
   p.sl2 = kLog2e / sqrtf(static_cast<float>(D));
@@ -643,17 +717,20 @@ cudaError_t run(const Kv4DecodeArgs& a, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(blocks));
   cudaError_t e = p.group <= 8 ? launch_main<D, 1>(p, grid, stream)
                                : launch_main<D, 2>(p, grid, stream);
-  if (e != cudaSuccess || p.splits == 1) return e;
-  return launch_pdl(kv4_join_kernel<D>, dim3(static_cast<unsigned>(rows)), dim3(32 * kJoinWarps), 0,
-                    stream, p);
+  if (e != cudaSuccess || p.splits == 1 || p.cluster) return e;
+  // few rows with many shares: the larger block reads more of them at once
+  const dim3 jgrid(static_cast<unsigned>(rows));
+  if (p.splits > 64)
+    return launch_pdl(kv4_join_kernel<D, 16>, jgrid, dim3(512), 0, stream, p);
+  return launch_pdl(kv4_join_kernel<D, 4>, jgrid, dim3(128), 0, stream, p);
 }
 
 }  // namespace
 
 size_t kv4_decode_workspace_bytes(const Kv4DecodeArgs& a) {
-  const int splits = splits_for(a);
-  if (splits == 1) return 0;
-  return static_cast<size_t>(a.batch) * a.heads * splits * (a.d + 2) * 4;
+  const Plan plan = plan_for(a);
+  if (plan.splits == 1 || plan.cluster) return 0;
+  return static_cast<size_t>(a.batch) * a.heads * plan.splits * (a.d + 2) * 4;
 }
 
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t stream) {
