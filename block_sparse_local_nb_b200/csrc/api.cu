@@ -178,9 +178,9 @@ nb_status kv4_rows(const void* k, const void* v, const void* cache, const int32_
   nb_status st = check_kv4(batch, kv_heads, d, max_pages, num_pages);
   if (st != NB_OK) return st;
   if (n < 0 || (dtype != NB_F32 && dtype != NB_BF16)) return NB_ERR_INVALID_ARG;
-  const double rows = static_cast<double>(batch) * kv_heads * n;
-  if (rows > INT32_MAX) return NB_ERR_UNSUPPORTED;
-  if (rows == 0) return NB_OK;
+  if (kv_heads > 65535 || batch > 65535) return NB_ERR_UNSUPPORTED;  // grid y / z limits
+  if (n > INT32_MAX - 64) return NB_ERR_UNSUPPORTED;
+  if (batch == 0 || n == 0) return NB_OK;
   // a table without pages maps nothing, so it and the pool may then be null
   if (!k || !v || (max_pages > 0 && !table) || (max_pages > 0 && num_pages > 0 && !cache))
     return NB_ERR_INVALID_ARG;

@@ -14,11 +14,12 @@
 // exact comparison: r = rint(estimate), k = r if r s <= x - m, else r - 1.
 // A group with a non-finite value (or a span beyond fp32) has s = m = NaN.
 //
-// A thread handles eight channels of the key row and of the value row of one
-// token; four neighbouring threads share a group.  The value codes are
-// transposed among eight lanes by three exchange steps.  Both kernels are
-// bound by memory: 2 d e + d + d / 4 bytes per token and head for both rows
-// (e = element size).
+// A thread handles sixteen channels of the key row and of the value row of one
+// token; two threads share a group, four transpose the value codes of 64 channels
+// among them.  (With eight channels a thread the kernels were bound by issued
+// instructions: 523 and 316 a warp of 512 values, 78 and 50 us for 4 x 8 heads x
+// 8192 x 128 bf16, where the bytes take 27 us each.)  Bytes per token and head for
+// both rows: 2 d e + d + d / 4 (e = element size).
 #include <cuda_bf16.h>
 
 #include "kv4.cuh"
@@ -50,24 +51,29 @@ __device__ __forceinline__ float bf16_below(float x) {
   return __uint_as_float((u & 0xffff0000u) + up);
 }
 
-struct Row8 {
-  float x[8];
+struct Row16 {
+  float x[16];
 };
 
 template <bool kF32>
-__device__ __forceinline__ Row8 load8(const void* p, int64_t at) {
-  Row8 r;
+__device__ __forceinline__ Row16 load16(const void* p, int64_t at) {
+  Row16 r;
   if constexpr (kF32) {
     const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    const float4 a = __ldcs(src), b = __ldcs(src + 1);
-    r.x[0] = a.x; r.x[1] = a.y; r.x[2] = a.z; r.x[3] = a.w;
-    r.x[4] = b.x; r.x[5] = b.y; r.x[6] = b.z; r.x[7] = b.w;
-  } else {
-    const uint4 a =
-        __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const float4 a = __ldcs(src + i);
+      r.x[4 * i] = a.x;
+      r.x[4 * i + 1] = a.y;
+      r.x[4 * i + 2] = a.z;
+      r.x[4 * i + 3] = a.w;
+    }
+  } else {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at);
+    const uint4 a = __ldcs(src), b = __ldcs(src + 1);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
       r.x[2 * i] = __uint_as_float(w[i] << 16);
       r.x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
@@ -75,78 +81,95 @@ __device__ __forceinline__ Row8 load8(const void* p, int64_t at) {
   return r;
 }
 
-// Eight codes of this thread (nibble i = channel i) and the group's param word.
-__device__ __forceinline__ uint32_t quantise8(const Row8& v, uint32_t& param) {
-  float lo = v.x[0], hi = v.x[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    lo = min_nan(lo, v.x[i]);
-    hi = max_nan(hi, v.x[i]);
-  }
-#pragma unroll
-  for (int off = 1; off < 4; off <<= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-  }
-  const float mid = bf16_below(__fadd_rd(0.5f * lo, 0.5f * hi));
-  const float half = max_nan(__fsub_ru(hi, mid), __fsub_ru(mid, lo));
-  if (!(half < __uint_as_float(0x7f800000u))) {  // NaN, infinity or overflow in the group
-    param = 0x7fc07fc0u;
-    return 0x88888888u;
-  }
-  // the estimate half / 7.5 is off by a few 2^-24, so the smallest bf16 whose
-  // 7.5-fold (exact) reaches half is its floor or one of the next two
-  const uint32_t c0 = __float_as_uint(half * (1.f / 7.5f)) & 0xffff0000u;
-  uint32_t su = c0;
-  if (7.5f * __uint_as_float(su) < half) su += 0x10000u;
-  if (7.5f * __uint_as_float(su) < half) su += 0x10000u;
-  param = (su >> 16) | (__float_as_uint(mid) & 0xffff0000u);
-  // steps near the bottom of the range are scaled up (exactly) for the reciprocal
-  const float f = __uint_as_float(su) < 0x1p-100f ? 0x1p+100f : 1.f;
-  const float s = __uint_as_float(su) * f;
-  const float inv = s > 0.f ? __frcp_rn(s) : 0.f;  // s = 0: every x is m
-  constexpr float kRint = 12582912.f;              // 1.5 * 2^23: adding it rounds to an integer
-  uint32_t w = 0;
+// Eight codes, nibble i = channel i.  The estimate z (-1 / s) of (x - m) / s is
+// rounded to an integer by adding 1.5 * 2^23 + 8, whose low bits then hold r + 8;
+// r s - (x - m) > 0 lowers it by one.  The constant's high bits go at the end.
+template <bool kTiny>
+__device__ __forceinline__ uint32_t codes8(const float* x, float mid, float s, float ninv) {
+  constexpr float kRint = 12582920.f;
+  constexpr uint32_t kBase = 0x4b400000u;
+  uint32_t w = 0u - (kBase + (kBase << 4) + (kBase << 8));  // further shifts leave nothing
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float y = __fsub_rd(v.x[i], mid) * f;
-    const float m = __fadd_rn(__fmul_rn(y, inv), kRint);
-    const float r = __fadd_rn(m, -kRint);
-    const bool over = __fmaf_rn(r, s, -y) > 0.f;  // r s > y, exactly
-    const uint32_t code = (__float_as_uint(m) + (over ? 7u : 8u)) & 15u;
-    w |= code << (4 * i);
+    float z = __fsub_ru(mid, x[i]);  // -(x - m rounded down)
+    if (kTiny) z *= 0x1p+100f;
+    const float m = __fmaf_rn(z, ninv, kRint);
+    uint32_t c = __float_as_uint(m);
+    if (__fmaf_rn(__fadd_rn(m, -kRint), s, z) > 0.f) --c;
+    w += c << (4 * i);
   }
   return w;
 }
 
-// Transposes the 8 x 8 nibbles held by eight neighbouring lanes (lane j nibble
-// i <-> lane i nibble j).
-__device__ __forceinline__ uint32_t transpose8(uint32_t w, int lane) {
-  uint32_t o = __shfl_xor_sync(0xffffffffu, w, 4);
-  w = (lane & 4) ? (w & 0xffff0000u) | (o >> 16) : (w & 0x0000ffffu) | (o << 16);
-  o = __shfl_xor_sync(0xffffffffu, w, 2);
-  w = (lane & 2) ? (w & 0xff00ff00u) | ((o >> 8) & 0x00ff00ffu)
-                 : (w & 0x00ff00ffu) | ((o & 0x00ff00ffu) << 8);
-  o = __shfl_xor_sync(0xffffffffu, w, 1);
-  return (lane & 1) ? (w & 0xf0f0f0f0u) | ((o >> 4) & 0x0f0f0f0fu)
-                    : (w & 0x0f0f0f0fu) | ((o & 0x0f0f0f0fu) << 4);
+// The codes of this thread's sixteen channels and the group's param word.
+__device__ __forceinline__ void quantise16(const Row16& v, uint32_t (&w)[2], uint32_t& param) {
+  float lo = v.x[0], hi = v.x[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) {
+    lo = min_nan(lo, v.x[i]);
+    hi = max_nan(hi, v.x[i]);
+  }
+  lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
+  hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
+  const float mid = bf16_below(__fadd_rd(0.5f * lo, 0.5f * hi));
+  const float half = max_nan(__fsub_ru(hi, mid), __fsub_ru(mid, lo));
+  if (!(half < __uint_as_float(0x7f800000u))) {  // NaN, infinity or overflow in the group
+    param = 0x7fc07fc0u;
+    w[0] = w[1] = 0x88888888u;
+    return;
+  }
+  // the estimate half / 7.5 is off by a few 2^-24, so the smallest bf16 whose
+  // 7.5-fold (exact) reaches half is its floor or one of the next two
+  uint32_t su = __float_as_uint(half * (1.f / 7.5f)) & 0xffff0000u;
+  if (7.5f * __uint_as_float(su) < half) su += 0x10000u;
+  if (7.5f * __uint_as_float(su) < half) su += 0x10000u;
+  param = (su >> 16) | (__float_as_uint(mid) & 0xffff0000u);
+  float s = __uint_as_float(su);
+  if (s >= 0x1p-100f || s == 0.f) {
+    const float ninv = s > 0.f ? __frcp_rn(-s) : 0.f;  // s = 0: every x is m
+    w[0] = codes8<false>(v.x, mid, s, ninv);
+    w[1] = codes8<false>(v.x + 8, mid, s, ninv);
+  } else {  // near the bottom of the range: scaled up (exactly) for the reciprocal
+    s *= 0x1p+100f;
+    const float ninv = __frcp_rn(-s);
+    w[0] = codes8<true>(v.x, mid, s, ninv);
+    w[1] = codes8<true>(v.x + 8, mid, s, ninv);
+  }
 }
 
-// Row `row` of a [batch][kv_heads][n] tensor, and where its token lives.
+// Transposes the 8 x 8 nibbles held by four neighbouring threads, words 2 j and
+// 2 j + 1 by thread j (word a nibble b <-> word b nibble a).
+__device__ __forceinline__ void transpose8(uint32_t (&w)[2], int lane) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t o = __shfl_xor_sync(0xffffffffu, w[i], 2);
+    w[i] = __byte_perm(w[i], o, (lane & 2) ? 0x3276u : 0x5410u);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t o = __shfl_xor_sync(0xffffffffu, w[i], 1);
+    w[i] = __byte_perm(w[i], o, (lane & 1) ? 0x3715u : 0x6240u);
+  }
+  const uint32_t a = w[0], b = w[1];
+  w[0] = (a & 0x0f0f0f0fu) | ((b & 0x0f0f0f0fu) << 4);
+  w[1] = (b & 0xf0f0f0f0u) | ((a >> 4) & 0x0f0f0f0fu);
+}
+
+// Where token t of sequence b lives.
 struct Slot {
   uint8_t* page;  // null: not one of the listed tokens, or not mapped
   int token;      // within the page
-  bool listed;    // row is one of the sequence's `count` tokens
+  bool listed;    // t is one of the sequence's `count` tokens
 };
 
 __device__ __forceinline__ Slot find_slot(const Pool& pool, const int32_t* starts,
-                                          const int32_t* counts, int n, int row, int page_bytes) {
+                                          const int32_t* counts, int b, int h, int t,
+                                          int page_bytes) {
   Slot s = {nullptr, 0, false};
-  const int bh = row / n, t = row - bh * n;
-  const int b = bh / pool.kv_heads, h = bh - b * pool.kv_heads;
+  const int start = starts ? starts[b] : 0;
   s.listed = counts == nullptr || t < counts[b];
   if (!s.listed) return s;
-  const int64_t pos = static_cast<int64_t>(starts ? starts[b] : 0) + t;
+  const int64_t pos = static_cast<int64_t>(start) + t;
   if (pos < 0 || pos >= static_cast<int64_t>(pool.max_pages) * kPage) return s;
   const int id = pool.table[static_cast<int64_t>(b) * pool.max_pages + (pos >> 5)];
   if (id < 0 || id >= pool.num_pages) return s;
@@ -155,121 +178,152 @@ __device__ __forceinline__ Slot find_slot(const Pool& pool, const int32_t* start
   return s;
 }
 
+// Places of thread j's words in a row: K words j and j + kGroups of the row's
+// first (its group g = j / 2, lane words t = 2 (j mod 2) and the next), V word
+// j / 4 of chunks r and r + 1, r = 2 (j mod 4).
+template <int D>
+struct Places {
+  using P = Page<D>;
+  uint8_t *k0, *k1, *v0, *v1;
+  uint32_t *kp, *vp;
+  __device__ __forceinline__ Places(uint8_t* page, int token, int j) {
+    const int g = j >> 1, t = 2 * (j & 1), r = 2 * (j & 3);
+    k0 = page + P::oK + token * P::kRow + (t * P::kGroups + g) * 4;
+    k1 = k0 + P::kGroups * 4;
+    uint8_t* v = page + P::oV + token * P::kRow + (j >> 2) * 4;
+    v0 = v + P::v_chunk(token, r);
+    v1 = v + P::v_chunk(token, r + 1);
+    kp = reinterpret_cast<uint32_t*>(page + P::oKPar + token * P::kParRow) + g;
+    vp = reinterpret_cast<uint32_t*>(page + P::oVPar + token * P::kParRow) + g;
+  }
+};
+
+template <int D>
+constexpr int kRows = kThreads / (D / 16);  // tokens of a block
+
+// Grid: blocks of tokens, heads, sequences.
 template <int D, bool kF32>
 __global__ void __launch_bounds__(kThreads)
     kv4_write_kernel(const void* k, const void* v, Pool pool, const int32_t* starts,
-                     const int32_t* counts, int n, int rows, int* err) {
-  using P = Page<D>;
-  constexpr int kLanes = D / 8;  // threads per row
+                     const int32_t* counts, int n, int* err) {
+  constexpr int kLanes = D / 16;  // threads per row
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, j = threadIdx.x % kLanes;
-  const int row = static_cast<int>(
-      (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) / kLanes);
+  const int t = blockIdx.x * kRows<D> + threadIdx.x / kLanes, h = blockIdx.y, b = blockIdx.z;
   Slot s = {nullptr, 0, false};
-  Row8 kr = {}, vr = {};
-  if (row < rows) {
-    s = find_slot(pool, starts, counts, n, row, P::kBytes);
-    if (s.page) {
-      const int64_t at = static_cast<int64_t>(row) * D + 8 * j;
-      kr = load8<kF32>(k, at);
-      vr = load8<kF32>(v, at);
-    } else if (s.listed && j == 0) {
-      sm100::record_error(err, kErrWriteSlot);
+  Row16 kr = {}, vr = {};
+  if (t < n) {
+    s = find_slot(pool, starts, counts, b, h, t, Page<D>::kBytes);
+    if (s.listed) {  // does not wait for the table
+      const int64_t at =
+          ((static_cast<int64_t>(b) * pool.kv_heads + h) * n + t) * D + 16 * j;
+      kr = load16<kF32>(k, at);
+      vr = load16<kF32>(v, at);
+      if (!s.page && j == 0) sm100::record_error(err, kErrWriteSlot);
     }
   }
-  uint32_t kpar, vpar;  // every lane takes part in the exchanges
-  const uint32_t kw = quantise8(kr, kpar);
-  const uint32_t vw = transpose8(quantise8(vr, vpar), lane);
+  uint32_t kw[2], vw[2], kpar, vpar;  // every lane takes part in the exchanges
+  quantise16(kr, kw, kpar);
+  quantise16(vr, vw, vpar);
+  transpose8(vw, lane);
   if (!s.page) return;
-  const int g = j >> 2, t = j & 3;
-  *reinterpret_cast<uint32_t*>(s.page + P::oK + s.token * P::kRow + (t * P::kGroups + g) * 4) = kw;
-  *reinterpret_cast<uint32_t*>(s.page + P::oV + s.token * P::kRow + P::v_chunk(s.token, j & 7) +
-                               (j >> 3) * 4) = vw;
-  if (t == 0) {
-    *reinterpret_cast<uint32_t*>(s.page + P::oKPar + s.token * P::kParRow + g * 4) = kpar;
-    *reinterpret_cast<uint32_t*>(s.page + P::oVPar + s.token * P::kParRow + g * 4) = vpar;
+  const Places<D> at(s.page, s.token, j);
+  *reinterpret_cast<uint32_t*>(at.k0) = kw[0];
+  *reinterpret_cast<uint32_t*>(at.k1) = kw[1];
+  if constexpr (D == 64) {  // the two chunks are neighbours
+    *reinterpret_cast<uint2*>(at.v0) = make_uint2(vw[0], vw[1]);
+  } else {
+    *reinterpret_cast<uint32_t*>(at.v0) = vw[0];
+    *reinterpret_cast<uint32_t*>(at.v1) = vw[1];
+  }
+  if ((j & 1) == 0) {
+    *at.kp = kpar;
+    *at.vp = vpar;
   }
 }
 
-// m + s (c - 7.5) for eight codes: s (c - 7.5) is exact inside the fused
-// multiply-add, so an fp32 output is rounded once.
+// m + s (c - 7.5) of eight codes, rounded once: in bf16 by one fused multiply-add
+// of exact bf16 operands, in fp32 likewise.
 template <bool kF32>
-__device__ __forceinline__ void store8(void* p, int64_t at, uint32_t w, uint32_t param,
-                                       bool zero) {
-  const float s = __uint_as_float(param << 16), m = __uint_as_float(param & 0xffff0000u);
-  float x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    // 2^23 + code - (2^23 + 7.5) would round; code - 7.5 through a shifted mantissa is exact:
-    // bits 0x4b000000 | 2 code is 2^23 + 2 code, minus 2^23 + 15 gives 2 (code - 7.5)
-    const uint32_t twice = i == 0 ? (w << 1) & 30u : (w >> (4 * i - 1)) & 30u;
-    const float c2 = __uint_as_float(0x4b000000u | twice) - 8388623.f;
-    x[i] = zero ? 0.f : fmaf(0.5f * s, c2, m);
-  }
+__device__ __forceinline__ void store8(void* p, int64_t at, uint32_t w, uint32_t param) {
   if constexpr (kF32) {
+    const float s = __uint_as_float(param << 16), m = __uint_as_float(param & 0xffff0000u);
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // the code doubled in the low bits of 2^23, minus 2^23 + 15: 2 (c - 7.5), exact
+      const uint32_t twice = i == 0 ? (w << 1) & 30u : (w >> (4 * i - 1)) & 30u;
+      x[i] = fmaf(0.5f * s, __uint_as_float(0x4b000000u | twice) - 8388623.f, m);
+    }
     float4* out = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
     __stcs(out, make_float4(x[0], x[1], x[2], x[3]));
     __stcs(out + 1, make_float4(x[4], x[5], x[6], x[7]));
   } else {
+    const uint32_t s2 = __byte_perm(param, 0, 0x1010), m2 = __byte_perm(param, 0, 0x3232);
+    const uint32_t c = 0x421e421eu;  // 39.5, 39.5
+    auto h2 = [](const uint32_t& x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // channels i and i + 4: 32 + c minus 39.5, exact
+      const uint32_t x = ((i == 0 ? w << 2 : w >> (4 * i - 2)) & 0x003c003cu) | 0x42004200u;
+      const __nv_bfloat162 r = __hfma2(__hsub2(h2(x), h2(c)), h2(s2), h2(m2));
+      y[i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
     __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at),
-           make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                      pack_bf16(x[6], x[7])));
+           make_uint4(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410),
+                      __byte_perm(y[0], y[1], 0x7632), __byte_perm(y[2], y[3], 0x7632)));
   }
 }
 
 template <int D, bool kF32>
 __global__ void __launch_bounds__(kThreads)
     kv4_read_kernel(void* k, void* v, Pool pool, const int32_t* starts, const int32_t* counts,
-                    int n, int rows, int* err) {
-  using P = Page<D>;
-  constexpr int kLanes = D / 8;
+                    int n, int* err) {
+  constexpr int kLanes = D / 16;
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, j = threadIdx.x % kLanes;
-  const int row = static_cast<int>(
-      (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) / kLanes);
-  const int g = j >> 2, t = j & 3;
-  Slot s = {nullptr, 0, false};
-  uint32_t kw = 0, vw = 0, kpar = 0, vpar = 0;
-  if (row < rows) {
-    s = find_slot(pool, starts, counts, n, row, P::kBytes);
+  const int t = blockIdx.x * kRows<D> + threadIdx.x / kLanes, h = blockIdx.y, b = blockIdx.z;
+  // codes 0 with s = m = 0 stand for 0: rows that are not listed or not mapped
+  uint32_t kw[2] = {0, 0}, vw[2] = {0, 0}, kpar = 0, vpar = 0;
+  if (t < n) {
+    const Slot s = find_slot(pool, starts, counts, b, h, t, Page<D>::kBytes);
     if (s.page) {
-      kw = *reinterpret_cast<const uint32_t*>(s.page + P::oK + s.token * P::kRow +
-                                              (t * P::kGroups + g) * 4);
-      vw = *reinterpret_cast<const uint32_t*>(s.page + P::oV + s.token * P::kRow +
-                                              P::v_chunk(s.token, j & 7) + (j >> 3) * 4);
-      kpar = *reinterpret_cast<const uint32_t*>(s.page + P::oKPar + s.token * P::kParRow + g * 4);
-      vpar = *reinterpret_cast<const uint32_t*>(s.page + P::oVPar + s.token * P::kParRow + g * 4);
+      const Places<D> at(s.page, s.token, j);
+      kw[0] = *reinterpret_cast<const uint32_t*>(at.k0);
+      kw[1] = *reinterpret_cast<const uint32_t*>(at.k1);
+      vw[0] = *reinterpret_cast<const uint32_t*>(at.v0);
+      vw[1] = *reinterpret_cast<const uint32_t*>(at.v1);
+      kpar = *at.kp;
+      vpar = *at.vp;
     } else if (s.listed && j == 0) {
       sm100::record_error(err, kErrReadSlot);
     }
   }
-  vw = transpose8(vw, lane);
-  if (row >= rows) return;
-  const int64_t at = static_cast<int64_t>(row) * D + 8 * j;
-  store8<kF32>(k, at, kw, kpar, !s.page);
-  store8<kF32>(v, at, vw, vpar, !s.page);
+  transpose8(vw, lane);
+  if (t >= n) return;
+  const int64_t at = ((static_cast<int64_t>(b) * pool.kv_heads + h) * n + t) * D + 16 * j;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    store8<kF32>(k, at + 8 * i, kw[i], kpar);
+    store8<kF32>(v, at + 8 * i, vw[i], vpar);
+  }
 }
 
 Pool make_pool(const Kv4Args& a) {
   return Pool{static_cast<uint8_t*>(a.cache), a.table, a.max_pages, a.num_pages, a.kv_heads};
 }
 
-unsigned blocks_for(const Kv4Args& a, int64_t rows) {
-  return static_cast<unsigned>((rows * (a.d / 8) + kThreads - 1) / kThreads);
-}
-
 template <int D, bool kF32>
 cudaError_t run(const Kv4Args& a, bool write, cudaStream_t stream) {
-  const int rows = a.batch * a.kv_heads * a.n;  // checked to fit by the caller
-  const dim3 grid(blocks_for(a, rows)), block(kThreads);
+  const dim3 grid((a.n + kRows<D> - 1) / kRows<D>, a.kv_heads, a.batch), block(kThreads);
   if (write)
     return launch_pdl(kv4_write_kernel<D, kF32>, grid, block, 0, stream,
                       static_cast<const void*>(a.k), static_cast<const void*>(a.v), make_pool(a),
-                      a.starts, a.counts, a.n, rows, a.err);
+                      a.starts, a.counts, a.n, a.err);
   return launch_pdl(kv4_read_kernel<D, kF32>, grid, block, 0, stream, a.k, a.v, make_pool(a),
-                    a.starts, a.counts, a.n, rows, a.err);
+                    a.starts, a.counts, a.n, a.err);
 }
 
 }  // namespace

@@ -370,7 +370,7 @@ NB_API size_t nb_kv4_page_bytes(int d);
  * A token whose position is negative, past max_pages pages or on an unmapped
  * page is skipped and reported (nb_kernel_error).  Two tokens of one call must
  * not share a slot (sequences that share a page must not both write to it).
- * batch * kv_heads * n must fit 31 bits (else NB_ERR_UNSUPPORTED).
+ * batch and kv_heads up to 65535 (more returns NB_ERR_UNSUPPORTED).
  */
 NB_API nb_status nb_kv4_write(const void* k, const void* v, void* cache, const int32_t* block_table,
                               const int32_t* starts, const int32_t* counts, int batch, int kv_heads,
