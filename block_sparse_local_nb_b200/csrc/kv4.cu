@@ -14,11 +14,11 @@
 // exact comparison: r = rint(estimate), k = r if r s <= x - m, else r - 1.
 // A group with a non-finite value (or a span beyond fp32) has s = m = NaN.
 //
-// A thread handles sixteen channels of the key row and of the value row of one
-// token; two threads share a group, four transpose the value codes of 64 channels
-// among them.  (With eight channels a thread the kernels were bound by issued
-// instructions: 523 and 316 a warp of 512 values, 78 and 50 us for 4 x 8 heads x
-// 8192 x 128 bf16, where the bytes take 27 us each.)  Bytes per token and head for
+// A writing thread handles sixteen channels of the key row and of the value row of
+// one token; two threads share a group, four transpose the value codes of 64 channels
+// among them.  (With eight channels a thread it was bound by issued instructions:
+// 523 a warp of 512 values, 78 us for 4 x 8 heads x 8192 x 128 bf16, where the
+// bytes take 27 us.)  Bytes per token and head for
 // both rows: 2 d e + d + d / 4 (e = element size).
 #include <cuda_bf16.h>
 
@@ -94,9 +94,11 @@ __device__ __forceinline__ uint32_t codes8(const float* x, float mid, float s, f
     float z = __fsub_ru(mid, x[i]);  // -(x - m rounded down)
     if (kTiny) z *= 0x1p+100f;
     const float m = __fmaf_rn(z, ninv, kRint);
-    uint32_t c = __float_as_uint(m);
-    if (__fmaf_rn(__fadd_rn(m, -kRint), s, z) > 0.f) --c;
-    w += c << (4 * i);
+    float over;  // 1 or 0: taking it off in fp32 spares the integer pipe, which is the busy one
+    asm("set.gt.f32.f32 %0, %1, 0f00000000;"
+        : "=f"(over)
+        : "f"(__fmaf_rn(__fadd_rn(m, -kRint), s, z)));
+    w += __float_as_uint(__fadd_rn(m, -over)) << (4 * i);
   }
   return w;
 }
@@ -155,21 +157,17 @@ __device__ __forceinline__ void transpose8(uint32_t (&w)[2], int lane) {
   w[1] = (b & 0xf0f0f0f0u) | ((a >> 4) & 0x0f0f0f0fu);
 }
 
-// Where token t of sequence b lives.
+// Where token t of a sequence's `count` lives.
 struct Slot {
   uint8_t* page;  // null: not one of the listed tokens, or not mapped
   int token;      // within the page
-  bool listed;    // t is one of the sequence's `count` tokens
 };
 
-__device__ __forceinline__ Slot find_slot(const Pool& pool, const int32_t* starts,
-                                          const int32_t* counts, int b, int h, int t,
-                                          int page_bytes) {
-  Slot s = {nullptr, 0, false};
-  const int start = starts ? starts[b] : 0;
-  s.listed = counts == nullptr || t < counts[b];
-  if (!s.listed) return s;
-  const int64_t pos = static_cast<int64_t>(start) + t;
+__device__ __forceinline__ Slot find_slot(const Pool& pool, const int32_t* starts, int b, int h,
+                                          int t, int count, int page_bytes) {
+  Slot s = {nullptr, 0};
+  if (t >= count) return s;
+  const int64_t pos = static_cast<int64_t>(starts ? starts[b] : 0) + t;
   if (pos < 0 || pos >= static_cast<int64_t>(pool.max_pages) * kPage) return s;
   const int id = pool.table[static_cast<int64_t>(b) * pool.max_pages + (pos >> 5)];
   if (id < 0 || id >= pool.num_pages) return s;
@@ -211,41 +209,38 @@ __global__ void __launch_bounds__(kThreads)
   pdl_wait();
   const int lane = threadIdx.x & 31, j = threadIdx.x % kLanes;
   const int t = blockIdx.x * kRows<D> + threadIdx.x / kLanes, h = blockIdx.y, b = blockIdx.z;
-  Slot s = {nullptr, 0, false};
-  Row16 kr = {}, vr = {};
-  if (t < n) {
-    s = find_slot(pool, starts, counts, b, h, t, Page<D>::kBytes);
-    if (s.listed) {  // does not wait for the table
-      const int64_t at =
-          ((static_cast<int64_t>(b) * pool.kv_heads + h) * n + t) * D + 16 * j;
-      kr = load16<kF32>(k, at);
-      vr = load16<kF32>(v, at);
-      if (!s.page && j == 0) sm100::record_error(err, kErrWriteSlot);
-    }
-  }
-  uint32_t kw[2], vw[2], kpar, vpar;  // every lane takes part in the exchanges
+  const int count = counts ? min(counts[b], n) : n;
+  if (!__any_sync(0xffffffffu, t < count)) return;
+  const Slot s = find_slot(pool, starts, b, h, t, count, Page<D>::kBytes);
+  // threads past the last token take its row along, for the exchanges
+  const int64_t at =
+      ((static_cast<int64_t>(b) * pool.kv_heads + h) * n + min(t, count - 1)) * D + 16 * j;
+  const Row16 kr = load16<kF32>(k, at), vr = load16<kF32>(v, at);
+  if (!s.page && t < count && j == 0) sm100::record_error(err, kErrWriteSlot);
+  uint32_t kw[2], vw[2], kpar, vpar;
   quantise16(kr, kw, kpar);
   quantise16(vr, vw, vpar);
   transpose8(vw, lane);
   if (!s.page) return;
-  const Places<D> at(s.page, s.token, j);
-  *reinterpret_cast<uint32_t*>(at.k0) = kw[0];
-  *reinterpret_cast<uint32_t*>(at.k1) = kw[1];
+  const Places<D> to(s.page, s.token, j);
+  *reinterpret_cast<uint32_t*>(to.k0) = kw[0];
+  *reinterpret_cast<uint32_t*>(to.k1) = kw[1];
   if constexpr (D == 64) {  // the two chunks are neighbours
-    *reinterpret_cast<uint2*>(at.v0) = make_uint2(vw[0], vw[1]);
+    *reinterpret_cast<uint2*>(to.v0) = make_uint2(vw[0], vw[1]);
   } else {
-    *reinterpret_cast<uint32_t*>(at.v0) = vw[0];
-    *reinterpret_cast<uint32_t*>(at.v1) = vw[1];
+    *reinterpret_cast<uint32_t*>(to.v0) = vw[0];
+    *reinterpret_cast<uint32_t*>(to.v1) = vw[1];
   }
   if ((j & 1) == 0) {
-    *at.kp = kpar;
-    *at.vp = vpar;
+    *to.kp = kpar;
+    *to.vp = vpar;
   }
 }
 
 // m + s (c - 7.5) of eight codes, rounded once: in bf16 by one fused multiply-add
-// of exact bf16 operands, in fp32 likewise.
-template <bool kF32>
+// of exact bf16 operands, in fp32 likewise.  Channel i is nibble i, or (kMixed)
+// nibble 4 (i mod 2) + i / 2, which puts neighbours four nibbles apart.
+template <bool kF32, bool kMixed>
 __device__ __forceinline__ void store8(void* p, int64_t at, uint32_t w, uint32_t param) {
   if constexpr (kF32) {
     const float s = __uint_as_float(param << 16), m = __uint_as_float(param & 0xffff0000u);
@@ -253,7 +248,8 @@ __device__ __forceinline__ void store8(void* p, int64_t at, uint32_t w, uint32_t
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       // the code doubled in the low bits of 2^23, minus 2^23 + 15: 2 (c - 7.5), exact
-      const uint32_t twice = i == 0 ? (w << 1) & 30u : (w >> (4 * i - 1)) & 30u;
+      const int nib = kMixed ? 4 * (i & 1) + (i >> 1) : i;
+      const uint32_t twice = nib == 0 ? (w << 1) & 30u : (w >> (4 * nib - 1)) & 30u;
       x[i] = fmaf(0.5f * s, __uint_as_float(0x4b000000u | twice) - 8388623.f, m);
     }
     float4* out = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
@@ -265,49 +261,81 @@ __device__ __forceinline__ void store8(void* p, int64_t at, uint32_t w, uint32_t
     auto h2 = [](const uint32_t& x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
     uint32_t y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // channels i and i + 4: 32 + c minus 39.5, exact
+    for (int i = 0; i < 4; ++i) {  // nibbles i and i + 4: 32 + c minus 39.5, exact
       const uint32_t x = ((i == 0 ? w << 2 : w >> (4 * i - 2)) & 0x003c003cu) | 0x42004200u;
       const __nv_bfloat162 r = __hfma2(__hsub2(h2(x), h2(c)), h2(s2), h2(m2));
       y[i] = *reinterpret_cast<const uint32_t*>(&r);
     }
-    __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at),
-           make_uint4(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410),
-                      __byte_perm(y[0], y[1], 0x7632), __byte_perm(y[2], y[3], 0x7632)));
+    uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at);
+    __stcs(out, kMixed ? make_uint4(y[0], y[1], y[2], y[3])
+                       : make_uint4(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410),
+                                    __byte_perm(y[0], y[1], 0x7632),
+                                    __byte_perm(y[2], y[3], 0x7632)));
   }
 }
 
+// Four threads read a token's rows back, one wide load each for codes and params:
+// thread j has K word [j][g], channels 32 g + 8 j .., of every group g, and V
+// chunks 2 j, 2 j + 1, whose words of 64 channels the four transpose among them
+// so that it ends with the same channels.  (A word a load was bound by the load
+// unit: 42 us for 4 x 8 x 8192 x 128.)
 template <int D, bool kF32>
 __global__ void __launch_bounds__(kThreads)
     kv4_read_kernel(void* k, void* v, Pool pool, const int32_t* starts, const int32_t* counts,
                     int n, int* err) {
-  constexpr int kLanes = D / 16;
+  using P = Page<D>;
+  constexpr int NG = P::kGroups;
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31, j = threadIdx.x % kLanes;
-  const int t = blockIdx.x * kRows<D> + threadIdx.x / kLanes, h = blockIdx.y, b = blockIdx.z;
+  const int lane = threadIdx.x & 31, j = threadIdx.x & 3;
+  const int t = blockIdx.x * (kThreads / 4) + threadIdx.x / 4, h = blockIdx.y, b = blockIdx.z;
   // codes 0 with s = m = 0 stand for 0: rows that are not listed or not mapped
-  uint32_t kw[2] = {0, 0}, vw[2] = {0, 0}, kpar = 0, vpar = 0;
+  uint32_t kw[NG] = {}, vw[NG] = {}, kpar[NG] = {}, vpar[NG] = {};
   if (t < n) {
-    const Slot s = find_slot(pool, starts, counts, b, h, t, Page<D>::kBytes);
+    const int count = counts ? min(counts[b], n) : n;
+    const Slot s = find_slot(pool, starts, b, h, t, count, P::kBytes);
     if (s.page) {
-      const Places<D> at(s.page, s.token, j);
-      kw[0] = *reinterpret_cast<const uint32_t*>(at.k0);
-      kw[1] = *reinterpret_cast<const uint32_t*>(at.k1);
-      vw[0] = *reinterpret_cast<const uint32_t*>(at.v0);
-      vw[1] = *reinterpret_cast<const uint32_t*>(at.v1);
-      kpar = *at.kp;
-      vpar = *at.vp;
-    } else if (s.listed && j == 0) {
+      auto load = [](uint32_t (&w)[NG], const uint8_t* p) {
+        if constexpr (NG == 4) {
+          const uint4 x = *reinterpret_cast<const uint4*>(p);
+          w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(p);
+          w[0] = x.x; w[1] = x.y;
+        }
+      };
+      load(kw, s.page + P::oK + s.token * P::kRow + j * (4 * NG));
+      load(vw, s.page + P::oV + s.token * P::kRow + P::v_chunk(s.token, 2 * j));
+      load(kpar, s.page + P::oKPar + s.token * P::kParRow);
+      load(vpar, s.page + P::oVPar + s.token * P::kParRow);
+    } else if (t < count && j == 0) {
       sm100::record_error(err, kErrReadSlot);
     }
   }
-  transpose8(vw, lane);
-  if (t >= n) return;
-  const int64_t at = ((static_cast<int64_t>(b) * pool.kv_heads + h) * n + t) * D + 16 * j;
+  // The words of chunks 2 j, 2 j + 1 (chunk bits j1 j0 e, word bit e its own), nibble
+  // bits n2 n1 n0: three exchanges bring n1 n0 to the thread and n2 to e, and leave
+  // nibble bits e j1 j0.
+  uint32_t vo[NG];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    store8<kF32>(k, at + 8 * i, kw[i], kpar);
-    store8<kF32>(v, at + 8 * i, vw[i], vpar);
+  for (int w = 0; w < NG / 2; ++w) {  // 64 channels each: vw = [chunk][word]
+    uint32_t x[2] = {vw[w], vw[NG / 2 + w]};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t o = __shfl_xor_sync(0xffffffffu, x[i], 2);
+      x[i] = __byte_perm(x[i], o, (lane & 2) ? 0x3715u : 0x6240u);
+      o = __shfl_xor_sync(0xffffffffu, x[i], 1);
+      x[i] = (lane & 1) ? (x[i] & 0xf0f0f0f0u) | ((o >> 4) & 0x0f0f0f0fu)
+                        : (x[i] & 0x0f0f0f0fu) | ((o & 0x0f0f0f0fu) << 4);
+    }
+    vo[2 * w] = __byte_perm(x[0], x[1], 0x5410);
+    vo[2 * w + 1] = __byte_perm(x[0], x[1], 0x7632);
+  }
+  if (t >= n) return;
+  const int64_t at = ((static_cast<int64_t>(b) * pool.kv_heads + h) * n + t) * D + 8 * j;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    store8<kF32, false>(k, at + 32 * g, kw[g], kpar[g]);
+    store8<kF32, true>(v, at + 32 * g, vo[g], vpar[g]);
   }
 }
 
@@ -317,7 +345,8 @@ Pool make_pool(const Kv4Args& a) {
 
 template <int D, bool kF32>
 cudaError_t run(const Kv4Args& a, bool write, cudaStream_t stream) {
-  const dim3 grid((a.n + kRows<D> - 1) / kRows<D>, a.kv_heads, a.batch), block(kThreads);
+  const int rows = write ? kRows<D> : kThreads / 4;  // tokens of a block
+  const dim3 grid((a.n + rows - 1) / rows, a.kv_heads, a.batch), block(kThreads);
   if (write)
     return launch_pdl(kv4_write_kernel<D, kF32>, grid, block, 0, stream,
                       static_cast<const void*>(a.k), static_cast<const void*>(a.v), make_pool(a),
