@@ -23,12 +23,15 @@
 //
 // The first key tile holds the sinks, which every later query of every head of
 // the group sees: up to group * n / 64 chunks against group * (window + 128) / 64
-// for another tile.  A tile's chunks are therefore cut into parts when they
-// exceed an SM's even share; parts are fp32 tiles in the workspace that the last
-// launch adds in order.
+// for another tile.  A tile's chunks are therefore cut into parts when they are
+// a large piece of an SM's even share; parts are fp32 tiles in the workspace that
+// the last launch adds in order.  The work items differ in cost, so a persistent
+// grid of one CTA per SM takes them from a counter in the workspace, the largest
+// first; which CTA takes an item does not change its result.
 //
 // Warp roles (512 threads, four warpgroups with reallocated registers): warp 0
-// TMA producer (a chunk that reaches past the length lands on a barrier of its
+// takes the items, decodes them for the others into a ring in shared memory, and
+// is the TMA producer (a chunk that reaches past the length lands on a barrier of its
 // own, and the warp zeroes the rows past it: P is 0 there, but 0 x NaN is not);
 // warp 1 TMEM owner and S/dP issuer; warp 2 issuer of the gradient products;
 // warpgroups 1 and 2 take the chunks in turn (thread = lane, 64 columns);
@@ -52,6 +55,8 @@ constexpr int kSlab = kRows * 128;        // swizzled box of the tile: 128 rows 
 constexpr int kChunkSlab = kChunk * 128;  // of a chunk
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxBatch = 1024;           // sequences in the shared-memory work table
+constexpr int kItems = 4;                 // items decoded ahead
+constexpr int kTakers = 14;               // arrivals that free one: 2 issuers, 8 + 4 warps
 
 struct Params {
   const void* o;
@@ -69,6 +74,7 @@ struct Params {
   int batch, heads, kv_heads, group, n, npad, ntiles, window, sinks;
   int s0, s1;    // parts of the first key tile, of another
   int items;     // of the main kernel
+  int* taken;    // items taken so far by the CTAs of <kDQ = false>, <kDQ = true>
   float scale;
 };
 
@@ -100,13 +106,16 @@ struct Cfg {
   static constexpr int oCh = oTile + NT * 2 * kTile;  // stage s: X at oCh + 2 s kHalf, Y after it
   static constexpr int oStg = oCh + NS * 2 * kHalf;   // output staging, one tile
   static constexpr int oCol = oStg + kTile;           // stage s: -lse log2 e and -D of its columns
-  static constexpr int oBar = oCol + (kDQ ? 0 : NS * 2 * kChunk * 4);
+  // kDQ: -lse log2 e and -D of the tile's rows, one set per tile buffer
+  static constexpr int oRow = oCol + (kDQ ? 0 : NS * 2 * kChunk * 4);
+  static constexpr int oItem = oRow + (kDQ ? NT * 2 * kRows * 4 : 0);  // ring of items
+  static constexpr int oBar = oItem + kItems * 64;
   static constexpr int bTFull = 0, bTFree = bTFull + NT, bCFull = bTFree + NT, bCFree = bCFull + NS,
                        bSFull = bCFree + NS, bSFree = bSFull + NSB, bPFull = bSFree + NSB,
-                       bAFull = bPFull + NSB, bAFree = bAFull + NACC, bFix = bAFree + NACC,
-                       bDone = bFix + 1, nBar = bDone + 1;
+                       bAFull = bPFull + NSB, bAFree = bAFull + NACC, bIFull = bAFree + NACC,
+                       bIFree = bIFull + kItems, bFix = bIFree + kItems, bDone = bFix + 1, nBar = bDone + 1;
   static constexpr int oSlot = oBar + nBar * 8;
-  static constexpr int oPre = oSlot + 16;             // work table: pre[0..batch], len[0..batch)
+  static constexpr int oPre = oSlot + 16;  // work table: pre[0..batch], len[0..batch)
   static constexpr int kSmem = oPre + (2 * kMaxBatch + 1) * 4 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
   static constexpr uint32_t kTmemCols = 512;
@@ -130,11 +139,12 @@ struct Item {
   int part, parts;    // key tiles: this item's part
 };
 
+// Items of a sequence of length L (kDQ: query tiles of all heads; else the key
+// tiles but the first, whose parts make a list of their own).
 template <bool kDQ>
 __device__ __forceinline__ int items_of(const Params& p, int L) {
   const int t = (L + kRows - 1) / kRows;
-  if (kDQ) return p.heads * t;
-  return t == 0 ? 0 : p.kv_heads * (p.s0 + (t - 1) * p.s1);
+  return kDQ ? p.heads * t : p.kv_heads * max(t - 1, 0) * p.s1;
 }
 
 // Warp-cooperative: prefix sums of the items per sequence, and the lengths.
@@ -161,71 +171,94 @@ __device__ void build_table(int* pre, const Params& p, int lane) {
   if (lane == 0) pre[0] = 0;
 }
 
-__device__ __forceinline__ int item_count(const Params& p, const int* pre) {
-  return p.batch <= kMaxBatch ? pre[p.batch] : p.items;
+// Parts of the first key tiles, at the head of the list.
+template <bool kDQ>
+__device__ __forceinline__ int first_items(const Params& p) {
+  return kDQ ? 0 : p.batch * p.kv_heads * p.s0;
 }
-
-// This CTA's item of round r; every second round runs backwards over the CTAs.
-__device__ __forceinline__ int item_at(int r) {
-  const int c = static_cast<int>(blockIdx.x), g = static_cast<int>(gridDim.x);
-  return r * g + ((r & 1) ? g - 1 - c : c);
+template <bool kDQ>
+__device__ __forceinline__ int item_count(const Params& p, const int* pre) {
+  return p.batch <= kMaxBatch ? first_items<kDQ>(p) + pre[p.batch] : p.items;
 }
 
 // Item k.  Heads are innermost; query tiles run from the last (most keys) to the
-// first, key tiles from the first (the sinks' parts).
+// first; key tiles begin with the parts of the first ones (the sinks').
 template <bool kDQ>
-__device__ __forceinline__ Item item(const Params& p, const int* pre, int k) {
+__device__ Item item(const Params& p, const int* pre, int k) {
   Item x;
-  int rem;
-  if (p.batch <= kMaxBatch) {
-    int lo = 0, hi = p.batch - 1;  // largest b with pre[b] <= k
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= k) lo = mid; else hi = mid - 1;
-    }
-    x.b = lo;
-    rem = k - pre[lo];
-    x.L = pre[kMaxBatch + 1 + lo];
-  } else {
-    const int per = p.items / p.batch;
-    x.b = k / per;
-    rem = k - x.b * per;
-    x.L = length_of(p, x.b);
-  }
-  const int heads = kDQ ? p.heads : p.kv_heads;
-  const int slot = rem / heads;
-  x.h = rem - slot * heads;
   x.c0 = x.nch = x.nq = x.k0 = x.far = x.part = 0;
   x.parts = 1;
+  const int lead = first_items<kDQ>(p);
+  if (k < lead) {
+    const int bkv = p.batch * p.kv_heads;
+    x.part = k / bkv;
+    x.parts = p.s0;
+    const int bh = k - x.part * bkv;
+    x.b = bh / p.kv_heads;
+    x.h = bh - x.b * p.kv_heads;
+    x.L = length_of(p, x.b);
+    x.tile = 0;
+  } else {
+    int rem = k - lead;
+    if (p.batch <= kMaxBatch) {
+      int lo = 0, hi = p.batch - 1;  // largest b with pre[b] <= rem
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= rem) lo = mid; else hi = mid - 1;
+      }
+      x.b = lo;
+      rem -= pre[lo];
+      x.L = pre[kMaxBatch + 1 + lo];
+    } else {
+      const int per = (p.items - lead) / p.batch;
+      x.b = rem / per;
+      rem -= x.b * per;
+      x.L = length_of(p, x.b);
+    }
+    const int heads = kDQ ? p.heads : p.kv_heads;
+    const int slot = rem / heads;
+    x.h = rem - slot * heads;
+    if (kDQ) {
+      x.tile = (p.batch <= kMaxBatch ? (x.L + kRows - 1) / kRows : p.ntiles) - 1 - slot;
+    } else {
+      x.tile = 1 + slot / p.s1;
+      x.part = slot % p.s1;
+      x.parts = p.s1;
+    }
+  }
+  const int r0 = x.tile * kRows;
+  if (r0 >= x.L) return x;
   if (kDQ) {
-    x.tile = (p.batch <= kMaxBatch ? (x.L + kRows - 1) / kRows : p.ntiles) - 1 - slot;
-    const int q0 = x.tile * kRows;
-    if (q0 >= x.L) return x;
-    x.k0 = q0 >= p.window ? q0 - p.window + 1 : 0;
+    x.k0 = r0 >= p.window ? r0 - p.window + 1 : 0;
     if (p.sinks > 0 && x.k0 > 0) {
       const int f = (p.sinks + kChunk - 1) / kChunk;
       if (x.k0 <= f * kChunk) x.k0 = 0;  // as many chunks either way
       else x.far = f;
     }
-    x.nch = x.far + (min(q0 + kRows, x.L) - x.k0 + kChunk - 1) / kChunk;
+    x.nch = x.far + (min(r0 + kRows, x.L) - x.k0 + kChunk - 1) / kChunk;
   } else {
-    if (slot < p.s0) {
-      x.tile = 0;
-      x.part = slot;
-      x.parts = p.s0;
-    } else {
-      const int t = (slot - p.s0) / p.s1;
-      x.tile = 1 + t;
-      x.part = slot - p.s0 - t * p.s1;
-      x.parts = p.s1;
-    }
-    if (x.tile * kRows >= x.L) return x;
     x.nq = query_chunks(x.tile, x.L, p.window, p.sinks);
     const int64_t all = static_cast<int64_t>(x.nq) * p.group;
     x.c0 = static_cast<int>(all * x.part / x.parts);
     x.nch = static_cast<int>(all * (x.part + 1) / x.parts) - x.c0;
   }
   return x;
+}
+
+// The rd-th item of this CTA from the ring, for every role but the producer;
+// x.nch < 0 after the last.  kWarp: called by a whole warp, whose lane 0 arrives.
+template <int D, bool kDQ, bool kWarp>
+__device__ __forceinline__ bool next_item(Item& x, int rd, uint32_t bar, const uint8_t* gbase,
+                                          int lane) {
+  using C = Cfg<D, kDQ>;
+  const int q = rd % kItems;
+  bool ok = mbar_wait(bar + 8 * (C::bIFull + q), (rd / kItems) & 1);
+  if (kWarp) ok = __all_sync(0xffffffffu, ok);
+  if (!ok) return false;
+  x = *reinterpret_cast<const Item*>(gbase + C::oItem + q * 64);
+  if (kWarp) __syncwarp();  // every lane has read it
+  if (lane == 0) mbar_arrive(bar + 8 * (C::bIFree + q));
+  return true;
 }
 
 // Chunk c of an item: its first row and the head it belongs to.
@@ -247,7 +280,7 @@ __device__ __forceinline__ Chunk chunk(const Params& p, const Item& x, int c) {
 }
 
 enum : int { kErrTFree = 0x81, kErrCFree, kErrFix, kErrTFull, kErrCFull, kErrSFree, kErrPFull,
-             kErrAFree, kErrSFull, kErrGCFull, kErrAFull, kErrDone };
+             kErrAFree, kErrSFull, kErrGCFull, kErrAFull, kErrDone, kErrIFree, kErrIFull, kErrGTFull };
 
 // Tiles and chunks (warp 0, the whole warp; lane 0 issues).
 template <int D, bool kDQ>
@@ -256,20 +289,45 @@ __device__ int producer(const Params& p, const int* pre, uint32_t base, uint8_t*
                         const CUtensorMap* cy) {
   using C = Cfg<D, kDQ>;
   const uint32_t bar = base + C::oBar;
-  const int count = item_count(p, pre);
+  const int count = item_count<kDQ>(p, pre);
   int g = 0, tc = 0, fixes = 0;
-  for (int rd = 0, it; (it = item_at(rd)) < count; ++rd) {
-    const Item x = item<kDQ>(p, pre, it);
-    if (x.nch == 0) continue;
+  int* taken = p.taken + (kDQ ? 1 : 0);
+  int fetched = lane == 0 ? atomicAdd(taken, 1) : 0;
+  for (int rd = 0;;) {
+    const int it = __shfl_sync(0xffffffffu, fetched, 0);
+    Item x;
+    if (it < count) {
+      if (lane == 0) fetched = atomicAdd(taken, 1);  // the next one, needed only after this
+      x = item<kDQ>(p, pre, it);
+      if (x.nch == 0) continue;
+    } else {
+      x.nch = -1;
+    }
+    const int q = rd % kItems;
+    if (!__all_sync(0xffffffffu,
+                    lane != 0 || mbar_wait(bar + 8 * (C::bIFree + q), ((rd / kItems) & 1) ^ 1)))
+      return kErrIFree;
+    if (lane == 0) {
+      *reinterpret_cast<Item*>(gbase + C::oItem + q * 64) = x;
+      mbar_arrive(bar + 8 * (C::bIFull + q));
+    }
+    ++rd;
+    if (x.nch < 0) break;
     const int tb = tc % C::NT;
     bool ok = true;
     if (lane == 0) {
       ok = mbar_wait(bar + 8 * (C::bTFree + tb), ((tc / C::NT) & 1) ^ 1);
       if (ok) {
         const uint32_t full = bar + 8 * (C::bTFull + tb);
-        mbar_arrive_expect_tx(full, 2 * C::kTile);
+        mbar_arrive_expect_tx(full, 2 * C::kTile + (kDQ ? 2 * kRows * 4 : 0));
         const uint32_t s = base + C::oTile + tb * 2 * C::kTile;
         const int bh = x.b * (kDQ ? p.heads : p.kv_heads) + x.h;
+        if (kDQ) {  // the rows' statistics, padded to whole tiles
+          const int64_t at = static_cast<int64_t>(bh) * p.npad + x.tile * kRows;
+          const uint32_t sr = base + C::oRow + tb * 2 * kRows * 4;
+          bulk_load(sr, p.nlse2 + at, kRows * 4, full);
+          bulk_load(sr + kRows * 4, p.nd + at, kRows * 4, full);
+        }
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
           tma_load_3d(s + i * kSlab, tx, full, i * 64, x.tile * kRows, bh);
@@ -324,15 +382,15 @@ __device__ int producer(const Params& p, const int* pre, uint32_t base, uint8_t*
 
 // S and dP of every chunk (warp 1, one thread).
 template <int D, bool kDQ>
-__device__ int s_issuer(const Params& p, const int* pre, uint32_t base, uint32_t tmem) {
+__device__ int s_issuer(const Params& p, uint32_t base, const uint8_t* gbase, uint32_t tmem) {
   using C = Cfg<D, kDQ>;
   const uint32_t bar = base + C::oBar;
   constexpr uint32_t kId = idesc_bf16_f32(128, kChunk, false, false);
-  const int count = item_count(p, pre);
   int g = 0, tc = 0;
-  for (int rd = 0, it; (it = item_at(rd)) < count; ++rd) {
-    const Item x = item<kDQ>(p, pre, it);
-    if (x.nch == 0) continue;
+  for (int rd = 0;; ++rd) {
+    Item x;
+    if (!next_item<D, kDQ, false>(x, rd, bar, gbase, 0)) return kErrIFull;
+    if (x.nch < 0) break;
     const int tb = tc % C::NT;
     const uint32_t sT = base + C::oTile + tb * 2 * C::kTile;
     const uint64_t dX = smem_desc_sw128(sT, 0, 1024), dY = smem_desc_sw128(sT + C::kTile, 0, 1024);
@@ -370,15 +428,15 @@ __device__ int s_issuer(const Params& p, const int* pre, uint32_t base, uint32_t
 // tensor memory, B = the chunk's rows (MN-major: 64-column atoms kChunkSlab
 // apart, 16 rows = 2048 bytes per step).
 template <int D, bool kDQ>
-__device__ int grad_issuer(const Params& p, const int* pre, uint32_t base, uint32_t tmem) {
+__device__ int grad_issuer(const Params& p, uint32_t base, const uint8_t* gbase, uint32_t tmem) {
   using C = Cfg<D, kDQ>;
   const uint32_t bar = base + C::oBar;
   constexpr uint32_t kId = idesc_bf16_f32(128, D, false, true);
-  const int count = item_count(p, pre);
   int g = 0, tc = 0;
-  for (int rd = 0, it; (it = item_at(rd)) < count; ++rd) {
-    const Item x = item<kDQ>(p, pre, it);
-    if (x.nch == 0) continue;
+  for (int rd = 0;; ++rd) {
+    Item x;
+    if (!next_item<D, kDQ, false>(x, rd, bar, gbase, 0)) return kErrIFull;
+    if (x.nch < 0) break;
     const int acc = tc % C::NACC;
     for (int c = 0; c < x.nch; ++c) {
       const int G = g + c, st = G % C::NS, sb = G % C::NSB;
@@ -423,7 +481,7 @@ __device__ __forceinline__ uint64_t bit_range(int64_t lo, int64_t hi) {
 
 // P and dS of the chunks of one warpgroup (every second chunk), thread = lane r.
 template <int D, bool kDQ>
-__device__ int grad_warps(const Params& p, const int* pre, uint32_t base, uint8_t* gbase,
+__device__ int grad_warps(const Params& p, uint32_t base, uint8_t* gbase,
                           uint32_t tmem, int wg, int wq, int lane) {
   using C = Cfg<D, kDQ>;
   const uint32_t bar = base + C::oBar;
@@ -431,17 +489,21 @@ __device__ int grad_warps(const Params& p, const int* pre, uint32_t base, uint8_
   const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16);
   const float sl2 = p.scale * kLog2e;
   auto all_ok = [](bool ok) { return __all_sync(0xffffffffu, ok); };
-  const int count = item_count(p, pre);
-  int g = 0;
-  for (int rd = 0, it; (it = item_at(rd)) < count; ++rd) {
-    const Item x = item<kDQ>(p, pre, it);
-    if (x.nch == 0) continue;
+  int g = 0, tc = 0;
+  for (int rd = 0;; ++rd) {
+    Item x;
+    if (!next_item<D, kDQ, true>(x, rd, bar, gbase, lane)) return kErrIFull;
+    if (x.nch < 0) break;
     const int row = x.tile * kRows + r;  // key (or query, kDQ) of this lane
     float nl_row = 0.f, nd_row = 0.f;
     if (kDQ) {
-      const int64_t at = (static_cast<int64_t>(x.b) * p.heads + x.h) * p.npad + row;
-      nl_row = p.nlse2[at];
-      nd_row = p.nd[at];
+      const int tb = tc % C::NT;
+      if (!all_ok(mbar_wait(bar + 8 * (C::bTFull + tb), (tc / C::NT) & 1))) return kErrGTFull;
+      const float* st = reinterpret_cast<const float*>(gbase + C::oRow + tb * 2 * kRows * 4);
+      nl_row = st[r];
+      nd_row = st[kRows + r];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar + 8 * (C::bTFree + tb));  // read; see the barrier's count
     }
     for (int c = (g & 1) ^ wg; c < x.nch; c += 2) {
       const int G = g + c, st = G % C::NS, sb = G % C::NSB;
@@ -521,6 +583,7 @@ __device__ int grad_warps(const Params& p, const int* pre, uint32_t base, uint8_
       mbar_arrive(bar + 8 * (C::bPFull + sb));
     }
     g += x.nch;
+    ++tc;
   }
   return 0;
 }
@@ -528,7 +591,7 @@ __device__ int grad_warps(const Params& p, const int* pre, uint32_t base, uint8_
 // Gradients of finished items (warpgroup 3, thread = lane r): bf16 tiles through
 // the staging buffer and a TMA store, or fp32 parts straight to the workspace.
 template <int D, bool kDQ>
-__device__ int epi_warps(const Params& p, const int* pre, uint32_t base, uint8_t* gbase,
+__device__ int epi_warps(const Params& p, uint32_t base, uint8_t* gbase,
                          uint32_t tmem, int wq, int lane, const CUtensorMap* to0,
                          const CUtensorMap* to1) {
   using C = Cfg<D, kDQ>;
@@ -537,11 +600,11 @@ __device__ int epi_warps(const Params& p, const int* pre, uint32_t base, uint8_t
   const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16);
   const bool leader = r == 0;
   auto all_ok = [](bool ok) { return __all_sync(0xffffffffu, ok); };
-  const int count = item_count(p, pre);
   int tc = 0;
-  for (int rd = 0, it; (it = item_at(rd)) < count; ++rd) {
-    const Item x = item<kDQ>(p, pre, it);
-    if (x.nch == 0) continue;
+  for (int rd = 0;; ++rd) {
+    Item x;
+    if (!next_item<D, kDQ, true>(x, rd, bar, gbase, lane)) return kErrIFull;
+    if (x.nch < 0) break;
     const int acc = tc % C::NACC;
     if (!all_ok(mbar_wait(bar + 8 * (C::bAFull + acc), (tc / C::NACC) & 1))) return kErrAFull;
     tc_fence_after();
@@ -627,7 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NT; ++i) {
       mbar_init(bar + 8 * (C::bTFull + i), 1);
-      mbar_init(bar + 8 * (C::bTFree + i), 1);
+      // the issuer's commit, and (kDQ) the eight warps that have read the row statistics
+      mbar_init(bar + 8 * (C::bTFree + i), kDQ ? 9 : 1);
     }
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(bar + 8 * (C::bCFull + i), 1);
@@ -641,6 +705,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < C::NACC; ++i) {
       mbar_init(bar + 8 * (C::bAFull + i), 1);
       mbar_init(bar + 8 * (C::bAFree + i), 128);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(bar + 8 * (C::bIFull + i), 1);
+      mbar_init(bar + 8 * (C::bIFree + i), kTakers);
     }
     mbar_init(bar + 8 * C::bFix, 1);
     mbar_init(bar + 8 * C::bDone, 2);  // one commit per MMA-issuing thread
@@ -670,14 +738,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     regs_dec<C::kRegsCtl, kLaunchRegs>();
     if (warp == 0) err = producer<D, kDQ>(p, pre, base, gbase, lane, &tx, &ty, &cx, &cy);
-    if (warp == 1 && lane == 0) err = s_issuer<D, kDQ>(p, pre, base, tmem);
-    if (warp == 2 && lane == 0) err = grad_issuer<D, kDQ>(p, pre, base, tmem);
+    if (warp == 1 && lane == 0) err = s_issuer<D, kDQ>(p, base, gbase, tmem);
+    if (warp == 2 && lane == 0) err = grad_issuer<D, kDQ>(p, base, gbase, tmem);
   } else if (warp < 12) {
     regs_inc<C::kRegsGrad, kLaunchRegs>();
-    err = grad_warps<D, kDQ>(p, pre, base, gbase, tmem, (warp - 4) >> 2, warp & 3, lane);
+    err = grad_warps<D, kDQ>(p, base, gbase, tmem, (warp - 4) >> 2, warp & 3, lane);
   } else {
     regs_dec<C::kRegsEpi, kLaunchRegs>();
-    err = epi_warps<D, kDQ>(p, pre, base, gbase, tmem, warp & 3, lane, &to0, &to1);
+    err = epi_warps<D, kDQ>(p, base, gbase, tmem, warp & 3, lane, &to0, &to1);
   }
   if (err) record_error(p.err, err);
 
@@ -695,53 +763,67 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Row statistics (padded to whole tiles), and zeros for the gradient rows of
-// tiles that lie past their sequence's length.
+// Row statistics (padded to whole tiles), zeros for the gradient rows of tiles
+// that lie past their sequence's length, and the counters of the main kernels.
+// Block = kRowsPer rows of one (sequence, head); a thread has eight elements
+// (16 bytes) of kPer rows, all loaded before the first is used.
+constexpr int kPer = 4;
+template <int D>
+constexpr int kRowsPer = kPer * 256 / (D / 8);  // 64 or 128: divides a tile
 template <int D>
 __global__ void __launch_bounds__(256) sink_rows_kernel(const Params p) {
-  constexpr int TPR = D / 8;  // threads per row, 8 elements (16 bytes) each
+  constexpr int TPR = D / 8, kStep = 256 / TPR;  // threads per row, rows at once
   pdl_trigger();
   pdl_wait();
-  const int64_t gt = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-  const int64_t row = gt / TPR;
-  const int part = static_cast<int>(gt % TPR);
-  const int64_t bh = row / p.npad;
-  const int q = static_cast<int>(row - bh * p.npad);
-  const bool in = bh < static_cast<int64_t>(p.batch) * p.heads;
-  float acc = 0.f;
-  bool valid = false;
-  if (in) {
-    const int b = static_cast<int>(bh / p.heads), h = static_cast<int>(bh - static_cast<int64_t>(b) * p.heads);
-    const int L = length_of(p, b);
-    valid = q < L;
-    if (valid) {
-      const int64_t at = (bh * p.n + q) * D + part * 8;
-      const uint4 ov = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.o) + at);
-      const uint4 dv = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dout) + at);
-      const __nv_bfloat162* o2 = reinterpret_cast<const __nv_bfloat162*>(&ov);
-      const __nv_bfloat162* d2 = reinterpret_cast<const __nv_bfloat162*>(&dv);
+  if (blockIdx.x == 0 && threadIdx.x < 2) p.taken[threadIdx.x] = 0;
+  const int per = p.npad / kRowsPer<D>;  // blocks per (sequence, head)
+  const int bh = static_cast<int>(blockIdx.x / per);
+  const int q0 = static_cast<int>(blockIdx.x - static_cast<unsigned>(bh) * per) * kRowsPer<D> +
+                 threadIdx.x / TPR;
+  const int part = threadIdx.x % TPR;
+  const int b = bh / p.heads, h = bh - b * p.heads;
+  const int L = length_of(p, b);
+  uint4 ov[kPer], dv[kPer];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 of = __bfloat1622float2(o2[i]);
-        const float2 df = __bfloat1622float2(d2[i]);
-        acc = fmaf(of.x, df.x, acc);
-        acc = fmaf(of.y, df.y, acc);
-      }
-    } else if (q < p.n && q / kRows * kRows >= L) {
-      const uint4 z = make_uint4(0, 0, 0, 0);
-      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dq) + (bh * p.n + q) * D)[part] = z;
-      if (h % p.group == 0) {
-        const int64_t kv = static_cast<int64_t>(b) * p.kv_heads + h / p.group;
-        reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dk) + (kv * p.n + q) * D)[part] = z;
-        reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dv) + (kv * p.n + q) * D)[part] = z;
-      }
+  for (int i = 0; i < kPer; ++i) {
+    const int q = q0 + i * kStep;
+    const int64_t at = (static_cast<int64_t>(bh) * p.n + q) * D + part * 8;
+    ov[i] = dv[i] = make_uint4(0, 0, 0, 0);
+    if (q < L) {
+      ov[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.o) + at);
+      dv[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dout) + at);
     }
   }
 #pragma unroll
-  for (int off = TPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-  if (in && part == 0) {
-    p.nd[row] = -acc;  // stored negated: the main kernels form dP + (-D)
-    p.nlse2[row] = valid ? -p.lse[bh * p.n + q] * kLog2e : -INFINITY;
+  for (int i = 0; i < kPer; ++i) {
+    const int q = q0 + i * kStep;
+    const __nv_bfloat162* o2 = reinterpret_cast<const __nv_bfloat162*>(&ov[i]);
+    const __nv_bfloat162* d2 = reinterpret_cast<const __nv_bfloat162*>(&dv[i]);
+    float acc = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 of = __bfloat1622float2(o2[e]);
+      const float2 df = __bfloat1622float2(d2[e]);
+      acc = fmaf(of.x, df.x, acc);
+      acc = fmaf(of.y, df.y, acc);
+    }
+#pragma unroll
+    for (int off = TPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+    if (part == 0) {
+      const int64_t row = static_cast<int64_t>(bh) * p.npad + q;
+      p.nd[row] = -acc;  // stored negated: the main kernels form dP + (-D)
+      p.nlse2[row] = q < L ? -p.lse[static_cast<int64_t>(bh) * p.n + q] * kLog2e : -INFINITY;
+    }
+    if (q < p.n && q / kRows * kRows >= L) {
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      const int64_t at = (static_cast<int64_t>(bh) * p.n + q) * D;
+      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dq) + at)[part] = z;
+      if (h % p.group == 0) {
+        const int64_t kv = ((static_cast<int64_t>(b) * p.kv_heads + h / p.group) * p.n + q) * D;
+        reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dk) + kv)[part] = z;
+        reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dv) + kv)[part] = z;
+      }
+    }
   }
 }
 
@@ -783,11 +865,13 @@ __global__ void __launch_bounds__(256) sink_join_kernel(const Params p, int tile
 
 struct Plan {
   int npad, ntiles, s0, s1;
-  int64_t nd, nlse2, part0, part1, bytes;  // workspace offsets and size
+  int64_t taken, nd, nlse2, part0, part1, bytes;  // workspace offsets and size
 };
 
-// Cuts key tiles into parts when one exceeds an SM's even share of all chunks
-// (never below 16 chunks a part: a part costs a tile of fp32 written and read).
+// Cuts key tiles into parts: the first ones when they are more than a third of an
+// SM's even share of all chunks (and larger than the others), the others when they
+// exceed that share; never below 16 chunks a part, which costs a tile of fp32
+// written and read.
 Plan make_plan(const SinkArgs& a) {
   Plan w;
   w.ntiles = (a.n + kRows - 1) / kRows;
@@ -802,16 +886,20 @@ Plan make_plan(const SinkArgs& a) {
   if (m > last) m = last;
   const int64_t all =
       c0 + group * (m * per + (last - m) * rest - (last * (last + 1) - m * (m + 1)));
-  int64_t cap = (all * bkv + 147) / 148;
-  if (cap < 16) cap = 16;
-  const int64_t s0 = (c0 + cap - 1) / cap, s1 = (c1 + cap - 1) / cap;
+  auto at_least = [](int64_t x, int64_t lo) { return x < lo ? lo : x; };
+  const int64_t share = (all * bkv + 147) / 148;
+  const int64_t cap1 = at_least(share, 16);
+  const int64_t s1 = (c1 + cap1 - 1) / cap1;
+  const int64_t cap0 = at_least(share / 3, at_least(s1 > 1 ? cap1 : c1, 16));
+  const int64_t s0 = (c0 + cap0 - 1) / cap0;
   w.s0 = static_cast<int>(s0 < 1 ? 1 : s0);
   w.s1 = static_cast<int>(s1 < 1 ? 1 : s1);
   const int64_t rows = static_cast<int64_t>(a.batch) * a.heads * w.npad;
   const int64_t tile = 2ll * kRows * a.d * 4;
-  w.nd = 0;
-  w.nlse2 = align_up(rows * 4, 256);
-  w.part0 = 2 * w.nlse2;
+  w.taken = 0;
+  w.nd = 256;
+  w.nlse2 = w.nd + align_up(rows * 4, 256);
+  w.part0 = w.nlse2 + align_up(rows * 4, 256);
   w.part1 = w.part0 + (w.s0 > 1 ? bkv * w.s0 * tile : 0);
   w.bytes = w.part1 + (w.s1 > 1 ? bkv * (w.ntiles - 1) * w.s1 * tile : 0);
   return w;
@@ -861,6 +949,7 @@ cudaError_t run(const SinkArgs& a, cudaStream_t stream) {
   p.dq = a.dq;
   p.dk = a.dk;
   p.dv = a.dv;
+  p.taken = reinterpret_cast<int*>(ws + w.taken);
   p.nd = reinterpret_cast<float*>(ws + w.nd);
   p.nlse2 = reinterpret_cast<float*>(ws + w.nlse2);
   p.part0 = reinterpret_cast<float*>(ws + w.part0);
@@ -878,8 +967,7 @@ cudaError_t run(const SinkArgs& a, cudaStream_t stream) {
   p.s0 = w.s0;
   p.s1 = w.s1;
   p.scale = a.scale;
-  const int64_t rows = static_cast<int64_t>(a.batch) * a.heads * w.npad;
-  const int64_t blocks = (rows * (D / 8) + 255) / 256;
+  const int64_t blocks = static_cast<int64_t>(a.batch) * a.heads * (w.npad / kRowsPer<D>);
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   cudaError_t e = launch_pdl(sink_rows_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
                              stream, p);
