@@ -17,9 +17,9 @@
 // S and dP are computed twice (7 products instead of 5), but every gradient is
 // accumulated in tensor memory in a fixed order: no fp32 accumulator of dQ in
 // global memory (cleared, added to with atomics and read back), and results
-// that repeat bit for bit.  P and dS overwrite S and dP in tensor memory and are
-// the A operands of the gradient products from there; neither passes through
-// shared memory.  Both are rounded to bf16 as operands.
+// that repeat bit for bit.  P and dS go back into tensor memory and are the A
+// operands of the gradient products from there; neither passes through shared
+// memory.  Both are rounded to bf16 as operands.
 //
 // The first key tile holds the sinks, which every later query of every head of
 // the group sees: up to group * n / 64 chunks against group * (window + 128) / 64
@@ -34,7 +34,10 @@
 // is the TMA producer (a chunk that reaches past the length lands on a barrier of its
 // own, and the warp zeroes the rows past it: P is 0 there, but 0 x NaN is not);
 // warp 1 TMEM owner and S/dP issuer; warp 2 issuer of the gradient products;
-// warpgroups 1 and 2 take the chunks in turn (thread = lane, 64 columns);
+// warpgroups 1 and 2 take the chunks in turn (thread = lane, 64 columns): a group
+// moves S and dP into registers and hands their columns back at once, so the next
+// chunk's products run under its arithmetic; P and dS have columns of their own
+// for each group;
 // warpgroup 3 epilogue (thread = lane), staging through swizzled shared memory
 // and TMA tensor stores.  Every wait is bounded (sm100.cuh).
 #include <math.h>
@@ -97,7 +100,7 @@ struct Cfg {
   // tiles that stay: two buffers at d = 64 (the next item's loads overlap), one at d = 128
   static constexpr int NT = D == 64 ? 2 : 1;
   static constexpr int NS = D == 64 ? 6 : 3;  // chunk stages
-  static constexpr int NSB = 2;               // S/dP buffers in tensor memory
+  static constexpr int NSB = kDQ && D == 64 ? 2 : 1;  // S/dP buffers in tensor memory
   static constexpr int NOUT = kDQ ? 1 : 2;    // gradients of an item
   static constexpr int NACC = D == 64 || kDQ ? 2 : 1;  // accumulator sets
   static constexpr int kTile = kRows * D * 2;
@@ -111,22 +114,26 @@ struct Cfg {
   static constexpr int oItem = oRow + (kDQ ? NT * 2 * kRows * 4 : 0);  // ring of items
   static constexpr int oBar = oItem + kItems * 64;
   static constexpr int bTFull = 0, bTFree = bTFull + NT, bCFull = bTFree + NT, bCFree = bCFull + NS,
-                       bSFull = bCFree + NS, bSFree = bSFull + NSB, bPFull = bSFree + NSB,
-                       bAFull = bPFull + NSB, bAFree = bAFull + NACC, bIFull = bAFree + NACC,
+                       bSFull = bCFree + NS, bSFree = bSFull + 2, bPFull = bSFree + NSB,
+                       bPFree = bPFull + 2, bAFull = bPFree + 2, bAFree = bAFull + NACC, bIFull = bAFree + NACC,
                        bIFree = bIFull + kItems, bFix = bIFree + kItems, bDone = bFix + 1, nBar = bDone + 1;
   static constexpr int oSlot = oBar + nBar * 8;
   static constexpr int oPre = oSlot + 16;  // work table: pre[0..batch], len[0..batch)
   static constexpr int kSmem = oPre + (2 * kMaxBatch + 1) * 4 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
   static constexpr uint32_t kTmemCols = 512;
-  // accumulators first, then the S/dP buffers (64 + 64 columns each)
+  // accumulators first, then the S/dP buffers (64 + 64 columns each), then each
+  // group's dS and P (32 columns each: 64 bf16)
   __device__ static constexpr uint32_t tAcc(int acc, int out) { return (acc * NOUT + out) * D; }
   static constexpr uint32_t tS0 = NACC * NOUT * D;
   __device__ static constexpr uint32_t tS(int sb) { return tS0 + sb * 2 * kChunk; }
-  static_assert(tS0 + NSB * 2 * kChunk <= kTmemCols, "tensor memory columns");
+  static constexpr uint32_t tP0 = tS0 + NSB * 2 * kChunk;
+  __device__ static constexpr uint32_t tDS(int pb) { return tP0 + pb * NOUT * (kChunk / 2); }
+  __device__ static constexpr uint32_t tP(int pb) { return tDS(pb) + kChunk / 2; }
+  static_assert(tP0 + 2 * NOUT * (kChunk / 2) <= kTmemCols, "tensor memory columns");
   static constexpr int kRegsCtl = 72;
-  static constexpr int kRegsGrad = 168;
-  static constexpr int kRegsEpi = 104;
+  static constexpr int kRegsGrad = 176;
+  static constexpr int kRegsEpi = 88;
   static_assert(128 * (kRegsCtl + 2 * kRegsGrad + kRegsEpi) <= kThreads * kLaunchRegs,
                 "register budget");
 };
@@ -280,7 +287,7 @@ __device__ __forceinline__ Chunk chunk(const Params& p, const Item& x, int c) {
 }
 
 enum : int { kErrTFree = 0x81, kErrCFree, kErrFix, kErrTFull, kErrCFull, kErrSFree, kErrPFull,
-             kErrAFree, kErrSFull, kErrGCFull, kErrAFull, kErrDone, kErrIFree, kErrIFull, kErrGTFull };
+             kErrAFree, kErrSFull, kErrGCFull, kErrAFull, kErrDone, kErrIFree, kErrIFull, kErrGTFull, kErrPFree };
 
 // Tiles and chunks (warp 0, the whole warp; lane 0 issues).
 template <int D, bool kDQ>
@@ -415,7 +422,7 @@ __device__ int s_issuer(const Params& p, uint32_t base, const uint8_t* gbase, ui
         const uint32_t oc = ((k >> 2) * kChunkSlab + (k & 3) * 32) >> 4;
         mma_bf16_ss(tS + kChunk, desc_add(dY, ot), desc_add(eY, oc), kId, k > 0);
       }
-      mma_commit(bar + 8 * (C::bSFull + sb));
+      mma_commit(bar + 8 * (C::bSFull + (G & 1)));  // one barrier per group, which sees all its phases
       if (c == x.nch - 1) mma_commit(bar + 8 * (C::bTFree + tb));  // the tile's only readers
     }
     g += x.nch;
@@ -439,15 +446,15 @@ __device__ int grad_issuer(const Params& p, uint32_t base, const uint8_t* gbase,
     if (x.nch < 0) break;
     const int acc = tc % C::NACC;
     for (int c = 0; c < x.nch; ++c) {
-      const int G = g + c, st = G % C::NS, sb = G % C::NSB;
+      const int G = g + c, st = G % C::NS, pb = G & 1;
       const uint32_t sC = base + C::oCh + st * 2 * C::kHalf;
       const uint64_t eX = smem_desc_sw128(sC, kChunkSlab, 1024);
       const uint64_t eY = smem_desc_sw128(sC + C::kHalf, kChunkSlab, 1024);
       if (c == 0 && !mbar_wait(bar + 8 * (C::bAFree + acc), ((tc / C::NACC) & 1) ^ 1))
         return kErrAFree;
-      if (!mbar_wait(bar + 8 * (C::bPFull + sb), (G / C::NSB) & 1)) return kErrPFull;
+      if (!mbar_wait(bar + 8 * (C::bPFull + pb), (G >> 1) & 1)) return kErrPFull;
       tc_fence_after();
-      const uint32_t tP = tmem + C::tS(sb), tDS = tP + kChunk;
+      const uint32_t tP = tmem + C::tP(pb), tDS = tmem + C::tDS(pb);
       const uint32_t out0 = tmem + C::tAcc(acc, 0);
       if (kDQ) {  // dQ += dS K
 #pragma unroll
@@ -462,7 +469,7 @@ __device__ int grad_issuer(const Params& p, uint32_t base, const uint8_t* gbase,
         for (int k = 0; k < kChunk / 16; ++k)
           mma_bf16_ts(out1, tDS + 8 * k, desc_add(eX, (k * 2048) >> 4), kId, c > 0 || k > 0);
       }
-      mma_commit(bar + 8 * (C::bSFree + sb));
+      mma_commit(bar + 8 * (C::bPFree + pb));
       mma_commit(bar + 8 * (C::bCFree + st));
       if (c == x.nch - 1) mma_commit(bar + 8 * (C::bAFull + acc));
     }
@@ -531,56 +538,76 @@ __device__ int grad_warps(const Params& p, uint32_t base, uint8_t* gbase,
       }
       if (!kDQ && !all_ok(mbar_wait(bar + 8 * (C::bCFull + st), (G / C::NS) & 1)))
         return kErrGCFull;
-      if (!all_ok(mbar_wait(bar + 8 * (C::bSFull + sb), (G / C::NSB) & 1))) return kErrSFull;
+      if (!all_ok(mbar_wait(bar + 8 * (C::bSFull + wg), (G >> 1) & 1))) return kErrSFull;
       tc_fence_after();
       const float* nl = reinterpret_cast<const float*>(gbase + C::oCol + st * 2 * kChunk * 4);
       const float* nd = nl + kChunk;
       const float2 sl = make_float2(sl2, sl2);
+      float s[2][32], dp[2][32];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        tmem_ld32(trow + C::tS(sb) + 32 * j, s[j]);
+        tmem_ld32(trow + C::tS(sb) + kChunk + 32 * j, dp[j]);
+      }
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        reg_fence(s[j]);
+        reg_fence(dp[j]);
+      }
+      tc_fence_before();
+      mbar_arrive(bar + 8 * (C::bSFree + sb));
+      // the products of this group's previous chunk have read its P and dS
+      if (!all_ok(mbar_wait(bar + 8 * (C::bPFree + wg), ((G >> 1) & 1) ^ 1))) return kErrPFree;
+      tc_fence_after();
 #pragma unroll
       for (int j = 0; j < 2; ++j) {  // 32 columns at a time
-        uint32_t wp[16], ws[16];
+        uint32_t wp[16], ws[16];  // P and dS of columns 2 i, 2 i + 1
         const uint32_t mw = static_cast<uint32_t>(mask >> (32 * j));
         if (whole || __any_sync(0xffffffffu, mw != 0u)) {
-          float s[32], dp[32];
-          tmem_ld32(trow + C::tS(sb) + 32 * j, s);
-          tmem_ld32(trow + C::tS(sb) + kChunk + 32 * j, dp);
-          tmem_wait_ld();
-          reg_fence(s);
-          reg_fence(dp);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {  // pairs of columns, packed fp32x2 arithmetic
-            float2 n2, d2;
+          for (int i = 0; i < 16; i += 2) {  // pairs of columns, packed fp32x2 arithmetic
+            float4 n4, d4;
             if (kDQ) {
-              n2 = make_float2(nl_row, nl_row);
-              d2 = make_float2(nd_row, nd_row);
+              n4 = make_float4(nl_row, nl_row, nl_row, nl_row);
+              d4 = make_float4(nd_row, nd_row, nd_row, nd_row);
             } else {
-              n2 = *reinterpret_cast<const float2*>(nl + 32 * j + 2 * i);
-              d2 = *reinterpret_cast<const float2*>(nd + 32 * j + 2 * i);
+              n4 = *reinterpret_cast<const float4*>(nl + 32 * j + 2 * i);
+              d4 = *reinterpret_cast<const float4*>(nd + 32 * j + 2 * i);
             }
-            const float2 e = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), sl, n2);
-            float2 pe = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-            float2 de = __fmul2_rn(pe, __fadd2_rn(make_float2(dp[2 * i], dp[2 * i + 1]), d2));
-            if (!whole) {  // selects, not products: a masked place may hold anything
-              const bool v0 = (mw >> (2 * i)) & 1u, v1 = (mw >> (2 * i + 1)) & 1u;
-              pe.x = v0 ? pe.x : 0.f;
-              pe.y = v1 ? pe.y : 0.f;
-              de.x = v0 ? de.x : 0.f;
-              de.y = v1 ? de.y : 0.f;
+            const float2 n2[2] = {make_float2(n4.x, n4.y), make_float2(n4.z, n4.w)};
+            const float2 d2[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int k = 2 * (i + e);
+              const float2 ex = __ffma2_rn(make_float2(s[j][k], s[j][k + 1]), sl, n2[e]);
+              const float2 pe = make_float2(ex2_approx(ex.x), ex2_approx(ex.y));
+              const float2 de =
+                  __fmul2_rn(pe, __fadd2_rn(make_float2(dp[j][k], dp[j][k + 1]), d2[e]));
+              wp[i + e] = pack_bf16(pe.x, pe.y);
+              ws[i + e] = pack_bf16(de.x, de.y);
             }
-            wp[i] = pack_bf16(pe.x, pe.y);
-            ws[i] = pack_bf16(de.x, de.y);
+          }
+          if (!whole && !__all_sync(0xffffffffu, mw == ~0u)) {
+            // masked places are cleared in the packed words: they may hold anything, NaN too
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t keep = ((mw >> (2 * i)) & 1u ? 0x0000ffffu : 0u) |
+                                    ((mw >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
+              wp[i] &= keep;
+              ws[i] &= keep;
+            }
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) wp[i] = ws[i] = 0u;
         }
-        // P and dS over the S and dP columns already read: columns 16 j .. 16 j + 15
-        if (!kDQ) tmem_st16u(trow + C::tS(sb) + 16 * j, wp);
-        tmem_st16u(trow + C::tS(sb) + kChunk + 16 * j, ws);
+        if (!kDQ) tmem_st16u(trow + C::tP(wg) + 16 * j, wp);
+        tmem_st16u(trow + C::tDS(wg) + 16 * j, ws);
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(bar + 8 * (C::bPFull + sb));
+      mbar_arrive(bar + 8 * (C::bPFull + wg));
     }
     g += x.nch;
     ++tc;
@@ -697,10 +724,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar + 8 * (C::bCFull + i), 1);
       mbar_init(bar + 8 * (C::bCFree + i), 1);
     }
-    for (int i = 0; i < C::NSB; ++i) {
+    for (int i = 0; i < C::NSB; ++i) mbar_init(bar + 8 * (C::bSFree + i), 128);
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar + 8 * (C::bSFull + i), 1);
-      mbar_init(bar + 8 * (C::bSFree + i), 1);
       mbar_init(bar + 8 * (C::bPFull + i), 128);
+      mbar_init(bar + 8 * (C::bPFree + i), 1);
     }
     for (int i = 0; i < C::NACC; ++i) {
       mbar_init(bar + 8 * (C::bAFull + i), 1);

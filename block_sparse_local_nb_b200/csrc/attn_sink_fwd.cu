@@ -59,7 +59,7 @@ template <int D>
 struct Cfg {
   static constexpr int NQ = D == 64 ? 2 : 1;   // Q tile buffers
   static constexpr int NKV = D == 64 ? 3 : 2;  // K chunk stages, and as many V chunk stages
-  static constexpr int NSB = D == 64 ? 3 : 2;  // S buffers
+  static constexpr int NSB = NKV;              // S buffers
   static constexpr int NOB = 1;  // O accumulators per half (tiles in flight)
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kKBytes = kChunk * D * 2;
@@ -70,10 +70,9 @@ struct Cfg {
   static constexpr int oBar = oStg + kRows * D * 2;
   // barrier indices ([S buffer][half] for P, [half][buffer] for O)
   static constexpr int bQFull = 0, bQFree = bQFull + NQ, bKFull = bQFree + NQ,
-                       bKFree = bKFull + NKV, bVFull = bKFree + NKV, bVFree = bVFull + NKV,
-                       bSFull = bVFree + NKV, bSFree = bSFull + NSB,
-                       bPFull = bSFree + NSB, bPVDone = bPFull + 2 * NSB, bOFull = bPVDone + 2 * NSB,
-                       bOFree = bOFull + 2 * NOB, bXFull = bOFree + 2 * NOB, bXFree = bXFull + 2,
+                       bVFull = bKFull + NKV, bSFull = bVFull + NKV, bSFree = bSFull + NSB,
+                       bPFull = bSFree + NSB, bOFull = bPFull + NSB, bOFree = bOFull + 1,
+                       bXFull = bOFree + 1, bXFree = bXFull + 2,
                        bVFix = bXFree + 2, bDone = bVFix + 1, nBar = bDone + 1;
   static constexpr int oSlot = oBar + nBar * 8;
   // per-tile hand-off of the halves' running max and sum to the epilogue warps:
@@ -189,7 +188,7 @@ __device__ int producer(const Params& p, const Sched& sch, uint32_t base, const 
                   s * 64, x.tile * kRows, bh);
     for (int c = 0; c < x.nch; ++c) {
       const int G = g + c, st = G % C::NKV;
-      if (!mbar_wait(bar + 8 * (C::bKFree + st), ((G / C::NKV) & 1) ^ 1)) return kErrKFree;
+      if (!mbar_wait(bar + 8 * (C::bSFull + st), ((G / C::NKV) & 1) ^ 1)) return kErrKFree;
       const uint32_t full = bar + 8 * (C::bKFull + st);
       mbar_arrive_expect_tx(full, C::kKBytes);
 #pragma unroll
@@ -222,7 +221,7 @@ __device__ int v_producer(const Params& p, const Sched& sch, uint32_t base, uint
       const uint32_t land = fix ? bar + 8 * C::bVFix : full;
       bool ok = true;
       if (lane == 0) {
-        ok = mbar_wait(bar + 8 * (C::bVFree + st), ((G / C::NKV) & 1) ^ 1);
+        ok = mbar_wait(bar + 8 * (C::bSFree + st), ((G / C::NKV) & 1) ^ 1);
         if (ok) {
           mbar_arrive_expect_tx(land, C::kKBytes);
 #pragma unroll
@@ -276,8 +275,7 @@ __device__ int s_issuer(const Params& p, const Sched& sch, uint32_t base, uint32
         const uint32_t off = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;  // descriptor address units
         mma_bf16_ss(tD, desc_add(dQ, off), desc_add(dK, off), kIdS, k > 0);
       }
-      mma_commit(bar + 8 * (C::bSFull + sb));
-      mma_commit(bar + 8 * (C::bKFree + st));  // the S product was this K chunk's only reader
+      mma_commit(bar + 8 * (C::bSFull + sb));  // also frees the K stage: its only reader
       if (c == x.nch - 1) mma_commit(bar + 8 * (C::bQFree + qs));  // the tile's S products issued
     }
     g += x.nch;
@@ -298,28 +296,24 @@ __device__ int pv_issuer(const Params& p, const Sched& sch, uint32_t base, uint3
   for (int rd = 0, it; (it = item_at(rd)) < sch.count; ++rd) {
     const Item x = sched_item(p, sch, it);
     if (x.nch == 0) continue;
-    const int ob = tc % C::NOB;
     for (int c = 0; c < x.nch; ++c) {
       const int G = g + c, st = G % C::NKV, sb = G % C::NSB;
       // V is MN-major: 64-column swizzle atoms kSlab apart, 8-key groups 1024 bytes apart
       const uint64_t dV = smem_desc_sw128(base + C::oV + st * C::kKBytes, kSlab, 1024);
       if (!mbar_wait(bar + 8 * (C::bVFull + st), (G / C::NKV) & 1)) return kErrVFull;
+      if (c == 0 && !mbar_wait(bar + 8 * C::bOFree, (tc & 1) ^ 1)) return kErrOFree;
+      if (!mbar_wait(bar + 8 * (C::bPFull + sb), (G / C::NSB) & 1)) return kErrPFull;
+      tc_fence_after();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // each half's 64 keys into its own O accumulator
-        const uint32_t tO = tmem + C::tO(h, ob), tP = tmem + C::tP(sb, h);
-        if (c == 0 &&
-            !mbar_wait(bar + 8 * (C::bOFree + h * C::NOB + ob), ((tc / C::NOB) & 1) ^ 1))
-          return kErrOFree;
-        if (!mbar_wait(bar + 8 * (C::bPFull + 2 * sb + h), (G / C::NSB) & 1)) return kErrPFull;
-        tc_fence_after();
+        const uint32_t tO = tmem + C::tO(h, 0), tP = tmem + C::tP(sb, h);
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // 16 keys = 8 P columns = 2048 bytes of V per step
           mma_bf16_ts(tO, tP + 8 * k, desc_add(dV, (h * 8192 + k * 2048) >> 4), kIdPV, c > 0 || k > 0);
-        mma_commit(bar + 8 * (C::bPVDone + 2 * sb + h));
-        if (c == x.nch - 1) mma_commit(bar + 8 * (C::bOFull + h * C::NOB + ob));
       }
+      // frees the S buffer and the V stage, and tells the softmax warps that O may be rescaled
       mma_commit(bar + 8 * (C::bSFree + sb));
-      mma_commit(bar + 8 * (C::bVFree + st));
+      if (c == x.nch - 1) mma_commit(bar + 8 * C::bOFull);
     }
     g += x.nch;
     ++tc;
@@ -443,7 +437,7 @@ __device__ int softmax_warps(const Params& p, const Sched& sch, uint32_t base, u
         // this half's previous P V product must have landed before its O is rescaled
         // (need implies c > 0, so chunk G - 1 belongs to this tile)
         const int Gp = G - 1;
-        if (!all_ok(mbar_wait(bar + 8 * (C::bPVDone + 2 * (Gp % C::NSB) + hf), (Gp / C::NSB) & 1)))
+        if (!all_ok(mbar_wait(bar + 8 * (C::bSFree + Gp % C::NSB), (Gp / C::NSB) & 1)))
           return kErrPPrev;
         tc_fence_after();
         const uint32_t to = trow + C::tO(hf, ob);
@@ -465,7 +459,7 @@ __device__ int softmax_warps(const Params& p, const Sched& sch, uint32_t base, u
       tmem_st32u(trow + C::tP(sb, hf), w);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(bar + 8 * (C::bPFull + 2 * sb + hf));
+      mbar_arrive(bar + 8 * (C::bPFull + sb));
     }
     // hand this half's (m, l) of the row to the epilogue warps
     const int par = tc & 1;
@@ -520,10 +514,7 @@ __device__ int epi_warps(const Params& p, const Sched& sch, uint32_t base, uint8
     const bool has = L > 0.f;  // padding rows and rows without a visible key: 0
     const float inv = has ? 1.f / L : 0.f;
     const float g0 = f0 * inv, g1 = f1 * inv;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (!all_ok(mbar_wait(bar + 8 * (C::bOFull + h * C::NOB + ob), (tc / C::NOB) & 1)))
-        return kErrOFull;
+    if (!all_ok(mbar_wait(bar + 8 * C::bOFull, tc & 1))) return kErrOFull;
     tc_fence_after();
     if (leader) bulk_wait_read0();  // the previous tile's store is done with the staging
     named_barrier(2, 128);
@@ -548,8 +539,7 @@ __device__ int epi_warps(const Params& p, const Sched& sch, uint32_t base, uint8
       }
     }
     tc_fence_before();
-    mbar_arrive(bar + 8 * (C::bOFree + 0 * C::NOB + ob));
-    mbar_arrive(bar + 8 * (C::bOFree + 1 * C::NOB + ob));
+    mbar_arrive(bar + 8 * C::bOFree);
     const int q = x.tile * kRows + r;
     if (q < a.n && a.lse) a.lse[bh * a.n + q] = has ? (M + log2f(L)) * kLn2 : -INFINITY;
     fence_proxy_async_smem();
@@ -586,25 +576,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < C::NKV; ++i) {
       mbar_init(bar + 8 * (C::bKFull + i), 1);
-      mbar_init(bar + 8 * (C::bKFree + i), 1);
       mbar_init(bar + 8 * (C::bVFull + i), 1);
-      mbar_init(bar + 8 * (C::bVFree + i), 1);
     }
     for (int i = 0; i < C::NSB; ++i) {
       mbar_init(bar + 8 * (C::bSFull + i), 1);
       mbar_init(bar + 8 * (C::bSFree + i), 1);
+      mbar_init(bar + 8 * (C::bPFull + i), 256);
     }
+    mbar_init(bar + 8 * C::bOFull, 1);
+    mbar_init(bar + 8 * C::bOFree, 128);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar + 8 * (C::bXFull + i), 256);
       mbar_init(bar + 8 * (C::bXFree + i), 128);
-    }
-    for (int i = 0; i < 2 * C::NSB; ++i) {
-      mbar_init(bar + 8 * (C::bPFull + i), 128);
-      mbar_init(bar + 8 * (C::bPVDone + i), 1);
-    }
-    for (int i = 0; i < 2 * C::NOB; ++i) {
-      mbar_init(bar + 8 * (C::bOFull + i), 1);
-      mbar_init(bar + 8 * (C::bOFree + i), 128);
     }
     mbar_init(bar + 8 * C::bVFix, 1);
     mbar_init(bar + 8 * C::bDone, 2);  // one commit per MMA-issuing thread
