@@ -11,6 +11,12 @@ allocation only; every step of the computation runs in ``libnb_b200.so``).
   integration (section 4 "Tech Stack"): forward through ``nb_attn_fwd``
   (keeping the log-sum-exp), backward through ``nb_attn_bwd`` (P recomputed
   from it).  Tensors are ``[batch, heads, n, d]``; the backward needs bf16.
+* :class:`SinkAttention` is the same for the causal attention with a sliding
+  window of tokens and visible first tokens (``nb_attn_sink_fwd`` and
+  ``nb_attn_sink_bwd``), with key/value heads that query heads may share.
+* :class:`KV4Cache` serves such a model token by token: a 4-bit key/value cache
+  (``nb_kv4_write``, ``nb_kv4_read``) and the single-token form of the attention
+  over it (``nb_attn_kv4_decode``).
 """
 
 from __future__ import annotations
@@ -112,3 +118,136 @@ class BlockSparseLocalAttention(torch.autograd.Function):
 def block_sparse_local_attention(q, k, v, lengths=None, R: int = 1, causal: bool = False):
     """Differentiable banded block-sparse local attention (see the class)."""
     return BlockSparseLocalAttention.apply(q, k, v, lengths, R, causal)
+
+
+class SinkAttention(torch.autograd.Function):
+    """O = softmax(Q K^T / sqrt(d)) V where query q sees key k when k <= q,
+    k < lengths[b] and (q - k < window or k < sinks), with its backward.  q is
+    [batch, heads, n, d], k and v [batch, kv_heads, n, d]; query head h reads
+    key/value head h // (heads // kv_heads)."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, lengths, window: int, sinks: int = 0):
+        if q.dim() != 4 or k.shape != v.shape or k.dim() != 4:
+            raise ValueError("q must be [batch, heads, n, d], k and v [batch, kv_heads, n, d]")
+        batch, heads, n, d = q.shape
+        if k.shape[0] != batch or k.shape[2:] != q.shape[2:]:
+            raise ValueError("q, k, v must share batch, n and d")
+        if not (q.dtype == k.dtype == v.dtype):
+            raise TypeError("q, k, v must share one dtype")
+        if not (q.device == k.device == v.device):
+            raise ValueError("q, k, v must be on one device")
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        if lengths is not None:
+            lengths = lengths.to(device=q.device, dtype=torch.int32).contiguous()
+        o = torch.empty_like(q)
+        lse = torch.empty((batch, heads, n), dtype=torch.float32, device=q.device)
+        with torch.cuda.device(q.device):
+            nb.nb_attn_sink_fwd(q, k, v, o, lse, lengths, batch, heads, k.shape[1], n, d, window,
+                                sinks, _dtype_code(q), torch.cuda.current_stream(q.device))
+        ctx.save_for_backward(q, k, v, o, lse, lengths)
+        ctx.window, ctx.sinks = window, sinks
+        return o
+
+    @staticmethod
+    def backward(ctx, do):
+        q, k, v, o, lse, lengths = ctx.saved_tensors
+        batch, heads, n, d = q.shape
+        do = do.to(q.dtype).contiguous()
+        shape = (batch, heads, k.shape[1], n, d, ctx.window, ctx.sinks, _dtype_code(q))
+        ws_bytes = nb.attn_sink_bwd_workspace_size(*shape)
+        ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=q.device)
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        with torch.cuda.device(q.device):
+            nb.nb_attn_sink_bwd(q, k, v, o, do, lse, lengths, dq, dk, dv, ws, ws_bytes, *shape,
+                                torch.cuda.current_stream(q.device))
+        return dq, dk, dv, None, None, None
+
+
+def sink_attention(q, k, v, lengths=None, window: int = 1, sinks: int = 0):
+    """Differentiable causal attention with a sliding window of tokens and visible
+    first tokens (see :class:`SinkAttention`)."""
+    return SinkAttention.apply(q, k, v, lengths, window, sinks)
+
+
+class KV4Cache:
+    """The 4-bit keys and values of a batch of sequences.
+
+    ``max_tokens`` bounds a sequence; its pages are taken from the pool in order,
+    so the block table is fixed.  ``lengths`` (int32 [batch], on the device) counts
+    the tokens of each sequence; ``append`` adds to it on the current stream, so a
+    captured step can be replayed.
+    """
+
+    def __init__(self, batch: int, kv_heads: int, d: int, max_tokens: int, device="cuda"):
+        page_bytes = nb.kv4_page_bytes(d)
+        if page_bytes == 0:
+            raise ValueError("d must be 64 or 128")
+        if batch < 1 or kv_heads < 1 or max_tokens < 1:
+            raise ValueError("batch, kv_heads and max_tokens must be positive")
+        self.batch, self.kv_heads, self.d = batch, kv_heads, d
+        self.device = torch.device(device)
+        self.max_pages = -(-max_tokens // BLOCK)
+        self.num_pages = batch * self.max_pages
+        self.pool = torch.zeros((self.num_pages, kv_heads, page_bytes), dtype=torch.uint8,
+                                device=self.device)
+        self.block_table = torch.arange(self.num_pages, dtype=torch.int32,
+                                        device=self.device).reshape(batch, self.max_pages)
+        self.lengths = torch.zeros(batch, dtype=torch.int32, device=self.device)
+
+    def _rows(self, x, name):
+        if x.dim() != 4 or x.shape[0] != self.batch or x.shape[1] != self.kv_heads or x.shape[3] != self.d:
+            raise ValueError(f"{name} must be [{self.batch}, {self.kv_heads}, n, {self.d}]")
+        return x.contiguous()
+
+    def append(self, k, v, counts=None):
+        """Quantise the first ``counts[b]`` (default: all n) tokens of k, v
+        [batch, kv_heads, n, d] behind those of sequence b.  Tokens past the
+        cache's end are dropped and reported by nb_kernel_error."""
+        k, v = self._rows(k, "k"), self._rows(v, "v")
+        if k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must share shape and dtype")
+        n = k.shape[2]
+        if counts is not None:
+            counts = counts.to(device=self.device, dtype=torch.int32).clamp(0, n).contiguous()
+        with torch.cuda.device(self.device):
+            nb.nb_kv4_write(k, v, self.pool, self.block_table, self.lengths, counts, self.batch,
+                            self.kv_heads, n, self.d, self.max_pages, self.num_pages,
+                            _dtype_code(k), torch.cuda.current_stream(self.device))
+            self.lengths.add_(n if counts is None else counts)
+
+    def read(self, n: int, starts=None, counts=None, dtype=torch.bfloat16):
+        """Tokens starts[b] .. starts[b] + n - 1 (default: from 0) as the cache holds
+        them, (k, v) [batch, kv_heads, n, d]; rows past counts[b] (default: the tokens
+        that the cache has from there) are 0."""
+        if starts is None:
+            starts = torch.zeros_like(self.lengths)
+        starts = starts.to(device=self.device, dtype=torch.int32).contiguous()
+        if counts is None:
+            counts = (self.lengths - starts).clamp(0, n)
+        counts = counts.to(device=self.device, dtype=torch.int32).contiguous()
+        k = torch.empty((self.batch, self.kv_heads, n, self.d), dtype=dtype, device=self.device)
+        v = torch.empty_like(k)
+        with torch.cuda.device(self.device):
+            nb.nb_kv4_read(self.pool, self.block_table, starts, counts, k, v, self.batch,
+                           self.kv_heads, n, self.d, self.max_pages, self.num_pages,
+                           _dtype_code(k), torch.cuda.current_stream(self.device))
+        return k, v
+
+    def attend(self, q, window: int = 2**31 - 1, sinks: int = 0):
+        """Attention of each sequence's last token, q [batch, heads, d] bf16, over its
+        window of tokens and its first ``sinks``; [batch, heads, d]."""
+        if q.dim() != 3 or q.shape[0] != self.batch or q.shape[2] != self.d:
+            raise ValueError(f"q must be [{self.batch}, heads, {self.d}]")
+        q = q.contiguous()
+        heads, code = q.shape[1], _dtype_code(q)
+        o = torch.empty_like(q)
+        size = nb.attn_kv4_decode_workspace_size(self.batch, heads, self.kv_heads, self.d,
+                                                 self.max_pages, window, sinks, code)
+        ws = torch.empty(size, dtype=torch.uint8, device=self.device) if size else None
+        with torch.cuda.device(self.device):
+            nb.nb_attn_kv4_decode(q, self.pool, self.block_table, self.lengths, o, None, ws, size,
+                                  self.batch, heads, self.kv_heads, self.d, self.max_pages,
+                                  self.num_pages, window, sinks, code,
+                                  torch.cuda.current_stream(self.device))
+        return o

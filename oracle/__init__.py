@@ -13,7 +13,7 @@ and softmax gradient) and sections 1, 2 and 5 (2-bit k-mer tokenizer, padding
 to a multiple of 32, the worked k-mer example).
 
 All floating point is fp64 (NumPy).  Every function is pinned by a CPU test in
-``tests/test_oracle_*.py`` against something other than itself (brute force,
+``tests/test_oracle_*.py`` and ``tests/test_serving_host.py`` against something other than itself (brute force,
 closed forms, invariants, finite differences, values printed on the page).
 """
 

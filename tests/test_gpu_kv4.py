@@ -274,3 +274,98 @@ def test_unmapped_positions_are_skipped_and_reported():
     assert nb.nb_kernel_error() == 0x51
     c.write(k.cuda(), v.cuda(), i32([90]), i32([7]))
     assert nb.nb_kernel_error() == 0x51  # position 96 is past the table
+
+
+def test_pool_offsets_past_32_bits():
+    """Pages whose byte offsets pass 2^32, reached through the table."""
+    num, d = 900_000, 128  # 4.6 GB
+    pool = torch.empty((num, 1, nb.kv4_page_bytes(d)), dtype=torch.uint8, device="cuda")
+    table = i32([[num - 1, 3, num - 2]])
+    k, v = (rows((1, 1, 90, d), s, torch.bfloat16) for s in (1, 2))
+    nb.nb_kv4_write(k.cuda(), v.cuda(), pool, table, None, None, 1, 1, 90, d, 3, num, nb.NB_BF16)
+    ko, vo = torch.empty(1, 1, 90, d, device="cuda"), torch.empty(1, 1, 90, d, device="cuda")
+    nb.nb_kv4_read(pool, table, None, None, ko, vo, 1, 1, 90, d, 3, num, nb.NB_F32)
+    kq, vq = kv4.values(k.double().numpy()), kv4.values(v.double().numpy())
+    assert np.array_equal(ko.cpu().numpy(), kq.astype(np.float32))
+    assert np.array_equal(vo.cpu().numpy(), vq.astype(np.float32))
+    q = torch.randn(1, 4, d, generator=torch.Generator().manual_seed(3)).bfloat16()
+    o, lse = torch.empty(1, 4, d, dtype=torch.bfloat16, device="cuda"), torch.empty(1, 4, device="cuda")
+    nb.nb_attn_kv4_decode(q.cuda(), pool, table, i32([90]), o, lse, None, 0, 1, 4, 1, d, 3, num, 90, 0,
+                          nb.NB_BF16)
+    want, want_lse = kv4.decode(q.double().numpy(), kq, vq, [90], 90, 0)
+    span = np.abs(vq).max()
+    assert (np.abs(o.double().cpu().numpy() - want) <= 2.0 ** -8 * (np.abs(want) + span) + 1e-4 * span).all()
+    assert np.abs(lse.double().cpu().numpy() - want_lse).max() <= 1e-4
+
+
+def test_no_pages_at_all():
+    """A table without pages: rows read as 0 and are reported; a decode gives 0."""
+    k = torch.ones(2, 1, 3, 64, dtype=torch.bfloat16, device="cuda")
+    nb.nb_kv4_write(k, k, None, None, None, None, 2, 1, 3, 64, 0, 0, nb.NB_BF16)
+    assert nb.nb_kernel_error() == 0x51
+    out = torch.ones_like(k)
+    nb.nb_kv4_read(None, None, None, None, out, out.clone(), 2, 1, 3, 64, 0, 0, nb.NB_BF16)
+    assert nb.nb_kernel_error() == 0x52 and (out == 0).all()
+    o = torch.ones(2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    nb.nb_attn_kv4_decode(o.clone(), None, None, None, o, None, None, 0, 2, 2, 1, 64, 0, 0, 5, 0, nb.NB_BF16)
+    assert (o == 0).all()
+
+
+def test_serving_from_prompt_to_tokens():
+    """The operators as a program uses them: a ragged prompt through the windowed
+    attention and into the cache, then tokens one by one through a captured step; each
+    token's output is the windowed attention's last row over what the cache reads back."""
+    from block_sparse_local_nb_b200.layer import KV4Cache, sink_attention
+    from oracle import sink
+
+    batch, heads, kv_heads, d, window, sinks = 3, 8, 2, 64, 70, 4
+    prompts, steps = [100, 33, 1], 40
+    n = max(prompts) + steps
+    g = torch.Generator().manual_seed(21)
+    q = torch.randn(batch, heads, n, d, generator=g).bfloat16().cuda()
+    k = rows((batch, kv_heads, n, d), 22, torch.bfloat16).cuda()
+    v = rows((batch, kv_heads, n, d), 23, torch.bfloat16).cuda()
+    L = i32(prompts)
+    p = max(prompts)
+    out = sink_attention(q[:, :, :p], k[:, :, :p], v[:, :, :p], L, window, sinks)
+    assert all((out[b, :, m:] == 0).all() for b, m in enumerate(prompts))
+    cache = KV4Cache(batch, kv_heads, d, n)
+    cache.append(k[:, :, :p], v[:, :, :p], L)
+    assert cache.lengths.tolist() == prompts
+    # sequence b's next tokens are its own rows prompts[b], prompts[b] + 1, ...
+    at = torch.tensor(prompts, device="cuda")
+    step_k = torch.empty(batch, kv_heads, 1, d, dtype=torch.bfloat16, device="cuda")
+    step_v, step_q = torch.empty_like(step_k), torch.empty(batch, heads, d, dtype=torch.bfloat16, device="cuda")
+    seq = torch.arange(batch, device="cuda")
+
+    def feed(i):
+        step_q.copy_(q[seq, :, at + i])
+        step_k.copy_(k[seq, :, at + i][:, :, None])
+        step_v.copy_(v[seq, :, at + i][:, :, None])
+
+    def step():
+        cache.append(step_k, step_v)
+        return cache.attend(step_q, window, sinks)
+
+    feed(0)
+    got = [step().clone()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        static = step()
+    for i in range(1, steps):
+        feed(i)
+        graph.replay()
+        got.append(static.clone())
+    torch.cuda.synchronize()
+    assert cache.lengths.tolist() == [m + steps for m in prompts]
+    kq, vq = cache.read(n, dtype=torch.float32)
+    ks, vs = kv4.values(k.double().cpu().numpy()), kv4.values(v.double().cpu().numpy())
+    for b, m in enumerate(prompts):
+        assert np.array_equal(kq[b, :, :m + steps].cpu().numpy(), ks[b, :, :m + steps].astype(np.float32))
+    span = np.abs(vs).max()
+    want, _ = sink.fwd(q.double().cpu().numpy(), ks, vs, window, sinks, [m + steps for m in prompts])
+    for i in range(steps):
+        for b, m in enumerate(prompts):
+            w = want[b, :, m + i]
+            off = np.abs(got[i][b].double().cpu().numpy() - w)
+            assert (off <= 2.0 ** -8 * (np.abs(w) + span) + 1e-4 * span).all()
