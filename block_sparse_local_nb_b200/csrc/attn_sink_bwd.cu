@@ -99,7 +99,7 @@ template <int D, bool kDQ>
 struct Cfg {
   // tiles that stay: two buffers at d = 64 (the next item's loads overlap), one at d = 128
   static constexpr int NT = D == 64 ? 2 : 1;
-  static constexpr int NS = D == 64 ? 6 : 3;  // chunk stages
+  static constexpr int NS = D == 64 ? 6 : 4;  // chunk stages (three at d = 128 wait for loads)
   static constexpr int NSB = kDQ && D == 64 ? 2 : 1;  // S/dP buffers in tensor memory
   static constexpr int NOUT = kDQ ? 1 : 2;    // gradients of an item
   static constexpr int NACC = D == 64 || kDQ ? 2 : 1;  // accumulator sets
@@ -107,8 +107,8 @@ struct Cfg {
   static constexpr int kHalf = kChunk * D * 2;   // one of the chunk's two operands
   static constexpr int oTile = 0;                // buffer i: X at oTile + 2 i kTile, Y after it
   static constexpr int oCh = oTile + NT * 2 * kTile;  // stage s: X at oCh + 2 s kHalf, Y after it
-  static constexpr int oStg = oCh + NS * 2 * kHalf;   // output staging, one tile
-  static constexpr int oCol = oStg + kTile;           // stage s: -lse log2 e and -D of its columns
+  static constexpr int oStg = oCh + NS * 2 * kHalf;   // output staging, 64 columns of a tile
+  static constexpr int oCol = oStg + kSlab;           // stage s: -lse log2 e and -D of its columns
   // kDQ: -lse log2 e and -D of the tile's rows, one set per tile buffer
   static constexpr int oRow = oCol + (kDQ ? 0 : NS * 2 * kChunk * 4);
   static constexpr int oItem = oRow + (kDQ ? NT * 2 * kRows * 4 : 0);  // ring of items
@@ -590,12 +590,20 @@ __device__ int grad_warps(const Params& p, uint32_t base, uint8_t* gbase,
           }
           if (!whole && !__all_sync(0xffffffffu, mw == ~0u)) {
             // masked places are cleared in the packed words: they may hold anything, NaN too
+            if (__all_sync(0xffffffffu, mw == ~0u || mw == 0u)) {  // whole rows (the sinks')
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint32_t keep = ((mw >> (2 * i)) & 1u ? 0x0000ffffu : 0u) |
-                                    ((mw >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
-              wp[i] &= keep;
-              ws[i] &= keep;
+              for (int i = 0; i < 16; ++i) {
+                wp[i] &= mw;
+                ws[i] &= mw;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const uint32_t keep = ((mw >> (2 * i)) & 1u ? 0x0000ffffu : 0u) |
+                                      ((mw >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
+                wp[i] &= keep;
+                ws[i] &= keep;
+              }
             }
           }
         } else {
@@ -647,48 +655,48 @@ __device__ int epi_warps(const Params& p, uint32_t base, uint8_t* gbase,
 #pragma unroll
     for (int out = 0; out < C::NOUT; ++out) {
       const float mul = kDQ || out == 1 ? p.scale : 1.f;  // dQ, dK; dV
-      if (part == nullptr) {
-        if (leader) bulk_wait_read0();  // the previous store is done with the staging
-        named_barrier(2, 128);
-      }
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        float v[32];
-        tmem_ld32(trow + C::tAcc(acc, out) + 32 * j, v);
-        tmem_wait_ld();
-        reg_fence(v);
+      for (int sl = 0; sl < D / 64; ++sl) {  // 64 columns at a time
+        if (part == nullptr) {
+          if (leader) bulk_wait_read0();  // the previous store is done with the staging
+          named_barrier(2, 128);
+        }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = valid ? v[i] * mul : 0.f;
-        if (part != nullptr) {
+        for (int j = 0; j < 2; ++j) {
+          const int col = 64 * sl + 32 * j;
+          float v[32];
+          tmem_ld32(trow + C::tAcc(acc, out) + col, v);
+          tmem_wait_ld();
+          reg_fence(v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(part + out * kRows * D + 32 * j + 4 * i) =
-                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else {
+          for (int i = 0; i < 32; ++i) v[i] = valid ? v[i] * mul : 0.f;
+          if (part != nullptr) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int gc = 4 * j + u;  // 16-byte chunk of the output row
-            *reinterpret_cast<uint4*>(gbase + C::oStg + (gc >> 3) * kSlab + r * 128 +
-                                      (((gc & 7) ^ (r & 7)) << 4)) =
-                make_uint4(pack_bf16(v[8 * u], v[8 * u + 1]), pack_bf16(v[8 * u + 2], v[8 * u + 3]),
-                           pack_bf16(v[8 * u + 4], v[8 * u + 5]),
-                           pack_bf16(v[8 * u + 6], v[8 * u + 7]));
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(part + out * kRows * D + col + 4 * i) =
+                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int gc = 4 * j + u;  // 16-byte chunk of the slab's row
+              *reinterpret_cast<uint4*>(gbase + C::oStg + r * 128 + ((gc ^ (r & 7)) << 4)) =
+                  make_uint4(pack_bf16(v[8 * u], v[8 * u + 1]), pack_bf16(v[8 * u + 2], v[8 * u + 3]),
+                             pack_bf16(v[8 * u + 4], v[8 * u + 5]),
+                             pack_bf16(v[8 * u + 6], v[8 * u + 7]));
+            }
           }
         }
-      }
-      if (out == C::NOUT - 1) {
-        tc_fence_before();
-        mbar_arrive(bar + 8 * (C::bAFree + acc));
-      }
-      if (part == nullptr) {
-        fence_proxy_async_smem();
-        named_barrier(1, 128);
-        if (leader) {
-#pragma unroll
-          for (int s = 0; s < D / 64; ++s)
-            tma_store_3d(out == 0 ? to0 : to1, base + C::oStg + s * kSlab, s * 64, x.tile * kRows,
-                         bh);
-          bulk_commit();
+        if (out == C::NOUT - 1 && sl == D / 64 - 1) {
+          tc_fence_before();
+          mbar_arrive(bar + 8 * (C::bAFree + acc));
+        }
+        if (part == nullptr) {
+          fence_proxy_async_smem();
+          named_barrier(1, 128);
+          if (leader) {
+            tma_store_3d(out == 0 ? to0 : to1, base + C::oStg, sl * 64, x.tile * kRows, bh);
+            bulk_commit();
+          }
         }
       }
     }
