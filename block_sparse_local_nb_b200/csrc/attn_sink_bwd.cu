@@ -100,9 +100,9 @@ struct Cfg {
   // tiles that stay: two buffers at d = 64 (the next item's loads overlap), one at d = 128
   static constexpr int NT = D == 64 ? 2 : 1;
   static constexpr int NS = D == 64 ? 6 : 4;  // chunk stages (three at d = 128 wait for loads)
-  static constexpr int NSB = kDQ && D == 64 ? 2 : 1;  // S/dP buffers in tensor memory
+  static constexpr int NSB = kDQ ? 2 : 1;     // S/dP buffers in tensor memory
   static constexpr int NOUT = kDQ ? 1 : 2;    // gradients of an item
-  static constexpr int NACC = D == 64 || kDQ ? 2 : 1;  // accumulator sets
+  static constexpr int NACC = D == 64 ? 2 : 1;  // accumulator sets
   static constexpr int kTile = kRows * D * 2;
   static constexpr int kHalf = kChunk * D * 2;   // one of the chunk's two operands
   static constexpr int oTile = 0;                // buffer i: X at oTile + 2 i kTile, Y after it
@@ -536,6 +536,9 @@ __device__ int grad_warps(const Params& p, uint32_t base, uint8_t* gbase,
           mask = row < x.L ? bit_range(row - col, (end < x.L ? end : x.L) - col) : 0ull;
         }
       }
+      // the products of this group's previous chunk have read its P and dS (long since:
+      // waiting here keeps the wait's own cost out of the chain from S to P)
+      if (!all_ok(mbar_wait(bar + 8 * (C::bPFree + wg), ((G >> 1) & 1) ^ 1))) return kErrPFree;
       if (!kDQ && !all_ok(mbar_wait(bar + 8 * (C::bCFull + st), (G / C::NS) & 1)))
         return kErrGCFull;
       if (!all_ok(mbar_wait(bar + 8 * (C::bSFull + wg), (G >> 1) & 1))) return kErrSFull;
@@ -557,9 +560,6 @@ __device__ int grad_warps(const Params& p, uint32_t base, uint8_t* gbase,
       }
       tc_fence_before();
       mbar_arrive(bar + 8 * (C::bSFree + sb));
-      // the products of this group's previous chunk have read its P and dS
-      if (!all_ok(mbar_wait(bar + 8 * (C::bPFree + wg), ((G >> 1) & 1) ^ 1))) return kErrPFree;
-      tc_fence_after();
 #pragma unroll
       for (int j = 0; j < 2; ++j) {  // 32 columns at a time
         uint32_t wp[16], ws[16];  // P and dS of columns 2 i, 2 i + 1
