@@ -252,18 +252,17 @@ __device__ Item item(const Params& p, const int* pre, int k) {
   return x;
 }
 
-// The rd-th item of this CTA from the ring, for every role but the producer;
-// x.nch < 0 after the last.  kWarp: called by a whole warp, whose lane 0 arrives.
-template <int D, bool kDQ, bool kWarp>
+// The rd-th item of this CTA from the ring, for the warps that work on it;
+// x.nch < 0 after the last.  Called by whole warps.
+template <int D, bool kDQ>
 __device__ __forceinline__ bool next_item(Item& x, int rd, uint32_t bar, const uint8_t* gbase,
                                           int lane) {
   using C = Cfg<D, kDQ>;
   const int q = rd % kItems;
-  bool ok = mbar_wait(bar + 8 * (C::bIFull + q), (rd / kItems) & 1);
-  if (kWarp) ok = __all_sync(0xffffffffu, ok);
-  if (!ok) return false;
+  if (!__all_sync(0xffffffffu, mbar_wait(bar + 8 * (C::bIFull + q), (rd / kItems) & 1)))
+    return false;
   x = *reinterpret_cast<const Item*>(gbase + C::oItem + q * 64);
-  if (kWarp) __syncwarp();  // every lane has read it
+  __syncwarp();  // every lane has read it
   if (lane == 0) mbar_arrive(bar + 8 * (C::bIFree + q));
   return true;
 }
@@ -387,46 +386,89 @@ __device__ int producer(const Params& p, const int* pre, uint32_t base, uint8_t*
   return 0;
 }
 
-// S and dP of every chunk (warp 1, one thread).
+// Number of chunks of the rd-th item, for the single-thread roles (the rest of the
+// item does not concern them); < 0 after the last, kNoItem on a timeout.
+constexpr int kNoItem = -2;
+template <int D, bool kDQ>
+__device__ __forceinline__ int next_chunks(int rd, uint32_t bar, const uint8_t* gbase) {
+  using C = Cfg<D, kDQ>;
+  const int q = rd % kItems;
+  if (!mbar_wait(bar + 8 * (C::bIFull + q), (rd / kItems) & 1)) return kNoItem;
+  const int nch = reinterpret_cast<const Item*>(gbase + C::oItem + q * 64)->nch;
+  mbar_arrive(bar + 8 * (C::bIFree + q));
+  return nch;
+}
+
+// Position in a ring of N barriers and the parity of its current pass.
+template <int N>
+struct Ring {
+  int i = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// Waits for two barriers, asking for both before looking at either answer.
+__device__ __forceinline__ int wait_both(uint32_t bar0, uint32_t ph0, uint32_t bar1, uint32_t ph1) {
+  const bool ok0 = mbar_try_wait(bar0, ph0), ok1 = mbar_try_wait(bar1, ph1);
+  if (!ok0 && !mbar_wait(bar0, ph0)) return 1;
+  if (!ok1 && !mbar_wait(bar1, ph1)) return 2;
+  return 0;
+}
+
+// S and dP of every chunk (warp 1, one thread).  A lone thread takes four cycles
+// and more an instruction, and what it does between two chunks is time the tensor
+// cores stand still: positions advance by steps, descriptors by adds.
 template <int D, bool kDQ>
 __device__ int s_issuer(const Params& p, uint32_t base, const uint8_t* gbase, uint32_t tmem) {
   using C = Cfg<D, kDQ>;
   const uint32_t bar = base + C::oBar;
   constexpr uint32_t kId = idesc_bf16_f32(128, kChunk, false, false);
-  int g = 0, tc = 0;
+  const uint64_t dX0 = smem_desc_sw128(base + C::oTile, 0, 1024);
+  const uint64_t dY0 = smem_desc_sw128(base + C::oTile + C::kTile, 0, 1024);
+  const uint64_t eX0 = smem_desc_sw128(base + C::oCh, 0, 1024);
+  const uint64_t eY0 = smem_desc_sw128(base + C::oCh + C::kHalf, 0, 1024);
+  Ring<C::NT> tile;
+  Ring<C::NS> ch;
+  Ring<C::NSB> sb;
+  int G = 0;
   for (int rd = 0;; ++rd) {
-    Item x;
-    if (!next_item<D, kDQ, false>(x, rd, bar, gbase, 0)) return kErrIFull;
-    if (x.nch < 0) break;
-    const int tb = tc % C::NT;
-    const uint32_t sT = base + C::oTile + tb * 2 * C::kTile;
-    const uint64_t dX = smem_desc_sw128(sT, 0, 1024), dY = smem_desc_sw128(sT + C::kTile, 0, 1024);
-    if (!mbar_wait(bar + 8 * (C::bTFull + tb), (tc / C::NT) & 1)) return kErrTFull;
-    for (int c = 0; c < x.nch; ++c) {
-      const int G = g + c, st = G % C::NS, sb = G % C::NSB;
-      const uint32_t sC = base + C::oCh + st * 2 * C::kHalf;
-      const uint64_t eX = smem_desc_sw128(sC, 0, 1024), eY = smem_desc_sw128(sC + C::kHalf, 0, 1024);
-      if (!mbar_wait(bar + 8 * (C::bCFull + st), (G / C::NS) & 1)) return kErrCFull;
-      if (!mbar_wait(bar + 8 * (C::bSFree + sb), ((G / C::NSB) & 1) ^ 1)) return kErrSFree;
+    const int nch = next_chunks<D, kDQ>(rd, bar, gbase);
+    if (nch == kNoItem) return kErrIFull;
+    if (nch < 0) break;
+    const uint32_t ot = tile.i * (2 * C::kTile >> 4);
+    if (!mbar_wait(bar + 8 * (C::bTFull + tile.i), tile.ph)) return kErrTFull;
+    for (int c = 0; c < nch; ++c, ++G) {
+      const uint32_t oc = ch.i * (2 * C::kHalf >> 4);
+      const uint64_t dX = desc_add(dX0, ot), dY = desc_add(dY0, ot);
+      const uint64_t eX = desc_add(eX0, oc), eY = desc_add(eY0, oc);
+      const int late = wait_both(bar + 8 * (C::bCFull + ch.i), ch.ph,
+                                 bar + 8 * (C::bSFree + sb.i), sb.ph ^ 1);
+      if (late) return late == 1 ? kErrCFull : kErrSFree;
       tc_fence_after();
-      const uint32_t tS = tmem + C::tS(sb);
+      const uint32_t tS = tmem + C::tS(sb.i);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const uint32_t ot = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
-        const uint32_t oc = ((k >> 2) * kChunkSlab + (k & 3) * 32) >> 4;
-        mma_bf16_ss(tS, desc_add(dX, ot), desc_add(eX, oc), kId, k > 0);
+        const uint32_t kt = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
+        const uint32_t kc = ((k >> 2) * kChunkSlab + (k & 3) * 32) >> 4;
+        mma_bf16_ss(tS, desc_add(dX, kt), desc_add(eX, kc), kId, k > 0);
       }
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const uint32_t ot = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
-        const uint32_t oc = ((k >> 2) * kChunkSlab + (k & 3) * 32) >> 4;
-        mma_bf16_ss(tS + kChunk, desc_add(dY, ot), desc_add(eY, oc), kId, k > 0);
+        const uint32_t kt = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
+        const uint32_t kc = ((k >> 2) * kChunkSlab + (k & 3) * 32) >> 4;
+        mma_bf16_ss(tS + kChunk, desc_add(dY, kt), desc_add(eY, kc), kId, k > 0);
       }
       mma_commit(bar + 8 * (C::bSFull + (G & 1)));  // one barrier per group, which sees all its phases
-      if (c == x.nch - 1) mma_commit(bar + 8 * (C::bTFree + tb));  // the tile's only readers
+      if (c == nch - 1) mma_commit(bar + 8 * (C::bTFree + tile.i));  // the tile's only readers
+      ch.next();
+      sb.next();
     }
-    g += x.nch;
-    ++tc;
+    tile.next();
   }
   return 0;
 }
@@ -439,29 +481,29 @@ __device__ int grad_issuer(const Params& p, uint32_t base, const uint8_t* gbase,
   using C = Cfg<D, kDQ>;
   const uint32_t bar = base + C::oBar;
   constexpr uint32_t kId = idesc_bf16_f32(128, D, false, true);
-  int g = 0, tc = 0;
+  const uint64_t eX0 = smem_desc_sw128(base + C::oCh, kChunkSlab, 1024);
+  const uint64_t eY0 = smem_desc_sw128(base + C::oCh + C::kHalf, kChunkSlab, 1024);
+  Ring<C::NACC> acc;
+  Ring<C::NS> ch;
+  Ring<2> pb;
   for (int rd = 0;; ++rd) {
-    Item x;
-    if (!next_item<D, kDQ, false>(x, rd, bar, gbase, 0)) return kErrIFull;
-    if (x.nch < 0) break;
-    const int acc = tc % C::NACC;
-    for (int c = 0; c < x.nch; ++c) {
-      const int G = g + c, st = G % C::NS, pb = G & 1;
-      const uint32_t sC = base + C::oCh + st * 2 * C::kHalf;
-      const uint64_t eX = smem_desc_sw128(sC, kChunkSlab, 1024);
-      const uint64_t eY = smem_desc_sw128(sC + C::kHalf, kChunkSlab, 1024);
-      if (c == 0 && !mbar_wait(bar + 8 * (C::bAFree + acc), ((tc / C::NACC) & 1) ^ 1))
-        return kErrAFree;
-      if (!mbar_wait(bar + 8 * (C::bPFull + pb), (G >> 1) & 1)) return kErrPFull;
+    const int nch = next_chunks<D, kDQ>(rd, bar, gbase);
+    if (nch == kNoItem) return kErrIFull;
+    if (nch < 0) break;
+    const uint32_t out0 = tmem + C::tAcc(acc.i, 0);
+    if (!mbar_wait(bar + 8 * (C::bAFree + acc.i), acc.ph ^ 1)) return kErrAFree;
+    for (int c = 0; c < nch; ++c) {
+      const uint32_t oc = ch.i * (2 * C::kHalf >> 4);
+      const uint64_t eX = desc_add(eX0, oc), eY = desc_add(eY0, oc);
+      const uint32_t tP = tmem + C::tP(pb.i), tDS = tmem + C::tDS(pb.i);
+      if (!mbar_wait(bar + 8 * (C::bPFull + pb.i), pb.ph)) return kErrPFull;
       tc_fence_after();
-      const uint32_t tP = tmem + C::tP(pb), tDS = tmem + C::tDS(pb);
-      const uint32_t out0 = tmem + C::tAcc(acc, 0);
       if (kDQ) {  // dQ += dS K
 #pragma unroll
         for (int k = 0; k < kChunk / 16; ++k)
           mma_bf16_ts(out0, tDS + 8 * k, desc_add(eX, (k * 2048) >> 4), kId, c > 0 || k > 0);
       } else {    // dV += P^T dO, dK += dS^T Q
-        const uint32_t out1 = tmem + C::tAcc(acc, C::NOUT - 1);
+        const uint32_t out1 = tmem + C::tAcc(acc.i, C::NOUT - 1);
 #pragma unroll
         for (int k = 0; k < kChunk / 16; ++k)
           mma_bf16_ts(out0, tP + 8 * k, desc_add(eY, (k * 2048) >> 4), kId, c > 0 || k > 0);
@@ -469,12 +511,13 @@ __device__ int grad_issuer(const Params& p, uint32_t base, const uint8_t* gbase,
         for (int k = 0; k < kChunk / 16; ++k)
           mma_bf16_ts(out1, tDS + 8 * k, desc_add(eX, (k * 2048) >> 4), kId, c > 0 || k > 0);
       }
-      mma_commit(bar + 8 * (C::bPFree + pb));
-      mma_commit(bar + 8 * (C::bCFree + st));
-      if (c == x.nch - 1) mma_commit(bar + 8 * (C::bAFull + acc));
+      mma_commit(bar + 8 * (C::bPFree + pb.i));
+      mma_commit(bar + 8 * (C::bCFree + ch.i));
+      if (c == nch - 1) mma_commit(bar + 8 * (C::bAFull + acc.i));
+      ch.next();
+      pb.next();
     }
-    g += x.nch;
-    ++tc;
+    acc.next();
   }
   return 0;
 }
@@ -499,7 +542,7 @@ __device__ int grad_warps(const Params& p, uint32_t base, uint8_t* gbase,
   int g = 0, tc = 0;
   for (int rd = 0;; ++rd) {
     Item x;
-    if (!next_item<D, kDQ, true>(x, rd, bar, gbase, lane)) return kErrIFull;
+    if (!next_item<D, kDQ>(x, rd, bar, gbase, lane)) return kErrIFull;
     if (x.nch < 0) break;
     const int row = x.tile * kRows + r;  // key (or query, kDQ) of this lane
     float nl_row = 0.f, nd_row = 0.f;
@@ -638,7 +681,7 @@ __device__ int epi_warps(const Params& p, uint32_t base, uint8_t* gbase,
   int tc = 0;
   for (int rd = 0;; ++rd) {
     Item x;
-    if (!next_item<D, kDQ, true>(x, rd, bar, gbase, lane)) return kErrIFull;
+    if (!next_item<D, kDQ>(x, rd, bar, gbase, lane)) return kErrIFull;
     if (x.nch < 0) break;
     const int acc = tc % C::NACC;
     if (!all_ok(mbar_wait(bar + 8 * (C::bAFull + acc), (tc / C::NACC) & 1))) return kErrAFull;
