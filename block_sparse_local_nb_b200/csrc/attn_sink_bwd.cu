@@ -53,9 +53,7 @@ using namespace sm100;
 constexpr int kThreads = 512;
 constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
 constexpr int kRows = 128;                // rows of the tile that stays
-constexpr int kChunk = 64;                // rows of a streamed chunk
 constexpr int kSlab = kRows * 128;        // swizzled box of the tile: 128 rows x 64 bf16
-constexpr int kChunkSlab = kChunk * 128;  // of a chunk
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxBatch = 1024;           // sequences in the shared-memory work table
 constexpr int kItems = 4;                 // items decoded ahead
@@ -86,23 +84,36 @@ __device__ __forceinline__ int length_of(const Params& p, int b) {
   return min(max(L, 0), p.n);
 }
 
+// Rows of a streamed chunk.  A product of 64 columns reads its 128-row operand from
+// shared memory for half the work (16 of them take 773 cycles, 16 of 128 columns
+// 1030), but 128 need room in tensor memory for S and dP of that width, and waste
+// more at the window's edges: they pay for dQ at d = 128 (252 -> 227 us at 8 heads x
+// 16384, window 2048; at d = 64 and window 160 dK and dV take 66 us with them, 54
+// without).
+constexpr int chunk_rows(int d, bool dq) { return dq && d == 128 ? 128 : 64; }
+
 // Chunks of queries that see key tile `tile` (per head), in a sequence of length L > 128 tile.
-__host__ __device__ __forceinline__ int query_chunks(int tile, int L, int window, int sinks) {
+__host__ __device__ __forceinline__ int query_chunks(int tile, int L, int window, int sinks,
+                                                     int chunk) {
   const int k0 = tile * kRows;
   // the last key of the tile is seen up to its window's end, the sinks by every query
   const int64_t far = static_cast<int64_t>(k0) + kRows - 1 + window;
   const int end = (tile == 0 && sinks > 0) || far > L ? L : static_cast<int>(far);
-  return (end - k0 + kChunk - 1) / kChunk;
+  return (end - k0 + chunk - 1) / chunk;
 }
 
 template <int D, bool kDQ>
 struct Cfg {
+  static constexpr int kChunk = chunk_rows(D, kDQ);
+  static constexpr bool kWide = kChunk == 128;  // both groups share every chunk, 64 columns each
+  static constexpr int kChunkSlab = kChunk * 128;  // swizzled box of a chunk
   // tiles that stay: two buffers at d = 64 (the next item's loads overlap), one at d = 128
   static constexpr int NT = D == 64 ? 2 : 1;
-  static constexpr int NS = D == 64 ? 6 : 4;  // chunk stages (three at d = 128 wait for loads)
-  static constexpr int NSB = kDQ ? 2 : 1;     // S/dP buffers in tensor memory
-  static constexpr int NOUT = kDQ ? 1 : 2;    // gradients of an item
-  static constexpr int NACC = D == 64 ? 2 : 1;  // accumulator sets
+  static constexpr int NS = D == 64 ? 6 : kWide ? 2 : 4;  // chunk stages
+  static constexpr int NSB = D == 64 && kDQ ? 2 : 1;      // S/dP buffers in tensor memory
+  static constexpr int NPB = 2;                           // P/dS buffers in tensor memory
+  static constexpr int NOUT = kDQ ? 1 : 2;                // gradients of an item
+  static constexpr int NACC = D == 64 ? 2 : 1;            // accumulator sets
   static constexpr int kTile = kRows * D * 2;
   static constexpr int kHalf = kChunk * D * 2;   // one of the chunk's two operands
   static constexpr int oTile = 0;                // buffer i: X at oTile + 2 i kTile, Y after it
@@ -115,22 +126,20 @@ struct Cfg {
   static constexpr int oBar = oItem + kItems * 64;
   static constexpr int bTFull = 0, bTFree = bTFull + NT, bCFull = bTFree + NT, bCFree = bCFull + NS,
                        bSFull = bCFree + NS, bSFree = bSFull + 2, bPFull = bSFree + NSB,
-                       bPFree = bPFull + 2, bAFull = bPFree + 2, bAFree = bAFull + NACC, bIFull = bAFree + NACC,
+                       bPFree = bPFull + NPB, bAFull = bPFree + NPB, bAFree = bAFull + NACC, bIFull = bAFree + NACC,
                        bIFree = bIFull + kItems, bFix = bIFree + kItems, bDone = bFix + 1, nBar = bDone + 1;
   static constexpr int oSlot = oBar + nBar * 8;
   static constexpr int oPre = oSlot + 16;  // work table: pre[0..batch], len[0..batch)
   static constexpr int kSmem = oPre + (2 * kMaxBatch + 1) * 4 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
   static constexpr uint32_t kTmemCols = 512;
-  // accumulators first, then the S/dP buffers (64 + 64 columns each), then each
-  // group's dS and P (32 columns each: 64 bf16)
+  // accumulators first, then S and dP, then dS and P (two bf16 per column)
   __device__ static constexpr uint32_t tAcc(int acc, int out) { return (acc * NOUT + out) * D; }
-  static constexpr uint32_t tS0 = NACC * NOUT * D;
-  __device__ static constexpr uint32_t tS(int sb) { return tS0 + sb * 2 * kChunk; }
-  static constexpr uint32_t tP0 = tS0 + NSB * 2 * kChunk;
+  static constexpr uint32_t tS0 = NACC * NOUT * D, tP0 = tS0 + NSB * 2 * kChunk;
+  __device__ static constexpr uint32_t tS(int sb) { return tS0 + sb * 2 * kChunk; }  // dP: + kChunk
   __device__ static constexpr uint32_t tDS(int pb) { return tP0 + pb * NOUT * (kChunk / 2); }
   __device__ static constexpr uint32_t tP(int pb) { return tDS(pb) + kChunk / 2; }
-  static_assert(tP0 + 2 * NOUT * (kChunk / 2) <= kTmemCols, "tensor memory columns");
+  static_assert(tP0 + NPB * NOUT * (kChunk / 2) <= kTmemCols, "tensor memory columns");
   static constexpr int kRegsCtl = 72;
   static constexpr int kRegsGrad = 176;
   static constexpr int kRegsEpi = 88;
@@ -190,8 +199,9 @@ __device__ __forceinline__ int item_count(const Params& p, const int* pre) {
 
 // Item k.  Heads are innermost; query tiles run from the last (most keys) to the
 // first; key tiles begin with the parts of the first ones (the sinks').
-template <bool kDQ>
+template <int D, bool kDQ>
 __device__ Item item(const Params& p, const int* pre, int k) {
+  constexpr int kChunk = chunk_rows(D, kDQ);
   Item x;
   x.c0 = x.nch = x.nq = x.k0 = x.far = x.part = 0;
   x.parts = 1;
@@ -244,7 +254,7 @@ __device__ Item item(const Params& p, const int* pre, int k) {
     }
     x.nch = x.far + (min(r0 + kRows, x.L) - x.k0 + kChunk - 1) / kChunk;
   } else {
-    x.nq = query_chunks(x.tile, x.L, p.window, p.sinks);
+    x.nq = query_chunks(x.tile, x.L, p.window, p.sinks, kChunk);
     const int64_t all = static_cast<int64_t>(x.nq) * p.group;
     x.c0 = static_cast<int>(all * x.part / x.parts);
     x.nch = static_cast<int>(all * (x.part + 1) / x.parts) - x.c0;
@@ -271,8 +281,9 @@ __device__ __forceinline__ bool next_item(Item& x, int rd, uint32_t bar, const u
 struct Chunk {
   int row, bh;
 };
-template <bool kDQ>
+template <int D, bool kDQ>
 __device__ __forceinline__ Chunk chunk(const Params& p, const Item& x, int c) {
+  constexpr int kChunk = chunk_rows(D, kDQ);
   Chunk k;
   if (kDQ) {
     k.row = c < x.far ? c * kChunk : x.k0 + (c - x.far) * kChunk;
@@ -286,7 +297,7 @@ __device__ __forceinline__ Chunk chunk(const Params& p, const Item& x, int c) {
 }
 
 enum : int { kErrTFree = 0x81, kErrCFree, kErrFix, kErrTFull, kErrCFull, kErrSFree, kErrPFull,
-             kErrAFree, kErrSFull, kErrGCFull, kErrAFull, kErrDone, kErrIFree, kErrIFull, kErrGTFull, kErrPFree };
+             kErrAFree, kErrSFull, kErrAFull, kErrDone, kErrIFree, kErrIFull, kErrGTFull };
 
 // Tiles and chunks (warp 0, the whole warp; lane 0 issues).
 template <int D, bool kDQ>
@@ -304,7 +315,7 @@ __device__ int producer(const Params& p, const int* pre, uint32_t base, uint8_t*
     Item x;
     if (it < count) {
       if (lane == 0) fetched = atomicAdd(taken, 1);  // the next one, needed only after this
-      x = item<kDQ>(p, pre, it);
+      x = item<D, kDQ>(p, pre, it);
       if (x.nch == 0) continue;
     } else {
       x.nch = -1;
@@ -344,25 +355,25 @@ __device__ int producer(const Params& p, const int* pre, uint32_t base, uint8_t*
     if (!__all_sync(0xffffffffu, ok)) return kErrTFree;
     for (int c = 0; c < x.nch; ++c) {
       const int G = g + c, st = G % C::NS;
-      const Chunk k = chunk<kDQ>(p, x, c);
-      const bool fix = k.row + kChunk > x.L && x.L < p.n;  // rows past the length hold other data
+      const Chunk k = chunk<D, kDQ>(p, x, c);
+      const bool fix = k.row + C::kChunk > x.L && x.L < p.n;  // rows past the length hold other data
       const uint32_t full = bar + 8 * (C::bCFull + st);
       const uint32_t land = fix ? bar + 8 * C::bFix : full;
       const uint32_t s = base + C::oCh + st * 2 * C::kHalf;
       if (lane == 0) {
         ok = mbar_wait(bar + 8 * (C::bCFree + st), ((G / C::NS) & 1) ^ 1);
         if (ok) {
-          mbar_arrive_expect_tx(land, 2 * C::kHalf + (kDQ ? 0 : 2 * kChunk * 4));
+          mbar_arrive_expect_tx(land, 2 * C::kHalf + (kDQ ? 0 : 2 * C::kChunk * 4));
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) {
-            tma_load_3d(s + i * kChunkSlab, cx, land, i * 64, k.row, k.bh);
-            tma_load_3d(s + C::kHalf + i * kChunkSlab, cy, land, i * 64, k.row, k.bh);
+            tma_load_3d(s + i * C::kChunkSlab, cx, land, i * 64, k.row, k.bh);
+            tma_load_3d(s + C::kHalf + i * C::kChunkSlab, cy, land, i * 64, k.row, k.bh);
           }
           if (!kDQ) {  // the columns' statistics, padded to whole tiles of 128
             const int64_t at = static_cast<int64_t>(k.bh) * p.npad + k.row;
-            const uint32_t sc = base + C::oCol + st * 2 * kChunk * 4;
-            bulk_load(sc, p.nlse2 + at, kChunk * 4, land);
-            bulk_load(sc + kChunk * 4, p.nd + at, kChunk * 4, land);
+            const uint32_t sc = base + C::oCol + st * 2 * C::kChunk * 4;
+            bulk_load(sc, p.nlse2 + at, C::kChunk * 4, land);
+            bulk_load(sc + C::kChunk * 4, p.nd + at, C::kChunk * 4, land);
           }
         }
       }
@@ -373,8 +384,8 @@ __device__ int producer(const Params& p, const int* pre, uint32_t base, uint8_t*
         uint4* v = reinterpret_cast<uint4*>(gbase + C::oCh + st * 2 * C::kHalf);
         // whole 128-byte rows of every box, so the swizzle does not matter
         for (int i = 0; i < 2 * (D / 64); ++i)
-          for (int j = (x.L - k.row) * 8 + lane; j < kChunk * 8; j += 32)
-            v[i * (kChunkSlab / 16) + j] = make_uint4(0, 0, 0, 0);
+          for (int j = (x.L - k.row) * 8 + lane; j < C::kChunk * 8; j += 32)
+            v[i * (C::kChunkSlab / 16) + j] = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(full);
@@ -404,9 +415,10 @@ template <int N>
 struct Ring {
   int i = 0;
   uint32_t ph = 0;
-  __device__ __forceinline__ void next() {
-    if (++i == N) {
-      i = 0;
+  __device__ __forceinline__ void next(int step = 1) {  // step <= N
+    i += step;
+    if (i >= N) {
+      i -= N;
       ph ^= 1;
     }
   }
@@ -427,7 +439,7 @@ template <int D, bool kDQ>
 __device__ int s_issuer(const Params& p, uint32_t base, const uint8_t* gbase, uint32_t tmem) {
   using C = Cfg<D, kDQ>;
   const uint32_t bar = base + C::oBar;
-  constexpr uint32_t kId = idesc_bf16_f32(128, kChunk, false, false);
+  constexpr uint32_t kId = idesc_bf16_f32(128, C::kChunk, false, false);
   const uint64_t dX0 = smem_desc_sw128(base + C::oTile, 0, 1024);
   const uint64_t dY0 = smem_desc_sw128(base + C::oTile + C::kTile, 0, 1024);
   const uint64_t eX0 = smem_desc_sw128(base + C::oCh, 0, 1024);
@@ -450,20 +462,21 @@ __device__ int s_issuer(const Params& p, uint32_t base, const uint8_t* gbase, ui
                                  bar + 8 * (C::bSFree + sb.i), sb.ph ^ 1);
       if (late) return late == 1 ? kErrCFull : kErrSFree;
       tc_fence_after();
-      const uint32_t tS = tmem + C::tS(sb.i);
+      const uint32_t tS = tmem + C::tS(sb.i), tDP = tS + C::kChunk;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint32_t kt = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
-        const uint32_t kc = ((k >> 2) * kChunkSlab + (k & 3) * 32) >> 4;
+        const uint32_t kc = ((k >> 2) * C::kChunkSlab + (k & 3) * 32) >> 4;
         mma_bf16_ss(tS, desc_add(dX, kt), desc_add(eX, kc), kId, k > 0);
       }
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint32_t kt = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
-        const uint32_t kc = ((k >> 2) * kChunkSlab + (k & 3) * 32) >> 4;
-        mma_bf16_ss(tS + kChunk, desc_add(dY, kt), desc_add(eY, kc), kId, k > 0);
+        const uint32_t kc = ((k >> 2) * C::kChunkSlab + (k & 3) * 32) >> 4;
+        mma_bf16_ss(tDP, desc_add(dY, kt), desc_add(eY, kc), kId, k > 0);
       }
-      mma_commit(bar + 8 * (C::bSFull + (G & 1)));  // one barrier per group, which sees all its phases
+      // groups that take turns have a barrier each, so that each sees all its phases
+      mma_commit(bar + 8 * (C::bSFull + (C::kWide ? 0 : G & 1)));
       if (c == nch - 1) mma_commit(bar + 8 * (C::bTFree + tile.i));  // the tile's only readers
       ch.next();
       sb.next();
@@ -474,18 +487,18 @@ __device__ int s_issuer(const Params& p, uint32_t base, const uint8_t* gbase, ui
 }
 
 // The gradient products of every chunk (warp 2, one thread): A = P or dS from
-// tensor memory, B = the chunk's rows (MN-major: 64-column atoms kChunkSlab
+// tensor memory, B = the chunk's rows (MN-major: 64-column atoms C::kChunkSlab
 // apart, 16 rows = 2048 bytes per step).
 template <int D, bool kDQ>
 __device__ int grad_issuer(const Params& p, uint32_t base, const uint8_t* gbase, uint32_t tmem) {
   using C = Cfg<D, kDQ>;
   const uint32_t bar = base + C::oBar;
   constexpr uint32_t kId = idesc_bf16_f32(128, D, false, true);
-  const uint64_t eX0 = smem_desc_sw128(base + C::oCh, kChunkSlab, 1024);
-  const uint64_t eY0 = smem_desc_sw128(base + C::oCh + C::kHalf, kChunkSlab, 1024);
+  const uint64_t eX0 = smem_desc_sw128(base + C::oCh, C::kChunkSlab, 1024);
+  const uint64_t eY0 = smem_desc_sw128(base + C::oCh + C::kHalf, C::kChunkSlab, 1024);
   Ring<C::NACC> acc;
   Ring<C::NS> ch;
-  Ring<2> pb;
+  Ring<C::NPB> pb;
   for (int rd = 0;; ++rd) {
     const int nch = next_chunks<D, kDQ>(rd, bar, gbase);
     if (nch == kNoItem) return kErrIFull;
@@ -500,15 +513,15 @@ __device__ int grad_issuer(const Params& p, uint32_t base, const uint8_t* gbase,
       tc_fence_after();
       if (kDQ) {  // dQ += dS K
 #pragma unroll
-        for (int k = 0; k < kChunk / 16; ++k)
+        for (int k = 0; k < C::kChunk / 16; ++k)
           mma_bf16_ts(out0, tDS + 8 * k, desc_add(eX, (k * 2048) >> 4), kId, c > 0 || k > 0);
       } else {    // dV += P^T dO, dK += dS^T Q
         const uint32_t out1 = tmem + C::tAcc(acc.i, C::NOUT - 1);
 #pragma unroll
-        for (int k = 0; k < kChunk / 16; ++k)
+        for (int k = 0; k < C::kChunk / 16; ++k)
           mma_bf16_ts(out0, tP + 8 * k, desc_add(eY, (k * 2048) >> 4), kId, c > 0 || k > 0);
 #pragma unroll
-        for (int k = 0; k < kChunk / 16; ++k)
+        for (int k = 0; k < C::kChunk / 16; ++k)
           mma_bf16_ts(out1, tDS + 8 * k, desc_add(eX, (k * 2048) >> 4), kId, c > 0 || k > 0);
       }
       mma_commit(bar + 8 * (C::bPFree + pb.i));
@@ -529,7 +542,8 @@ __device__ __forceinline__ uint64_t bit_range(int64_t lo, int64_t hi) {
   return b > a ? (~0ull >> (64 - (b - a))) << a : 0ull;
 }
 
-// P and dS of the chunks of one warpgroup (every second chunk), thread = lane r.
+// P and dS of 64 columns of a chunk a warpgroup: half of every chunk (wide chunks),
+// or every second chunk.  Thread = lane r.
 template <int D, bool kDQ>
 __device__ int grad_warps(const Params& p, uint32_t base, uint8_t* gbase,
                           uint32_t tmem, int wg, int wq, int lane) {
@@ -539,61 +553,83 @@ __device__ int grad_warps(const Params& p, uint32_t base, uint8_t* gbase,
   const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16);
   const float sl2 = p.scale * kLog2e;
   auto all_ok = [](bool ok) { return __all_sync(0xffffffffu, ok); };
-  int g = 0, tc = 0;
+  // this group's chunks: all (wide), or those of its parity, counted over all items
+  constexpr int kStep = C::kWide ? 1 : 2;
+  int G = C::kWide ? 0 : wg, g = 0;  // its next chunk, and the item's first
+  Ring<C::NS> ch;                    // chunk G's stage, S/dP buffer, P/dS buffer; the
+  Ring<C::NSB> sb;                   // parity of its own S barrier is full.ph
+  Ring<C::NPB> pb;
+  Ring<1> full;
+  if (!C::kWide && wg) {
+    ch.next();
+    sb.next();
+    pb.next();
+  }
+  const int half = C::kWide ? 64 * wg : 0;  // this group's 64 columns of a chunk
+  const uint32_t sfull = bar + 8 * (C::bSFull + (C::kWide ? 0 : wg));
+  Ring<C::NT> tile;
   for (int rd = 0;; ++rd) {
     Item x;
     if (!next_item<D, kDQ>(x, rd, bar, gbase, lane)) return kErrIFull;
     if (x.nch < 0) break;
-    const int row = x.tile * kRows + r;  // key (or query, kDQ) of this lane
+    const int t0 = x.tile * kRows, row = t0 + r;  // row: key (or query, kDQ) of this lane
     float nl_row = 0.f, nd_row = 0.f;
     if (kDQ) {
-      const int tb = tc % C::NT;
-      if (!all_ok(mbar_wait(bar + 8 * (C::bTFull + tb), (tc / C::NT) & 1))) return kErrGTFull;
-      const float* st = reinterpret_cast<const float*>(gbase + C::oRow + tb * 2 * kRows * 4);
+      if (!all_ok(mbar_wait(bar + 8 * (C::bTFull + tile.i), tile.ph))) return kErrGTFull;
+      const float* st = reinterpret_cast<const float*>(gbase + C::oRow + tile.i * 2 * kRows * 4);
       nl_row = st[r];
       nd_row = st[kRows + r];
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar + 8 * (C::bTFree + tb));  // read; see the barrier's count
+      if (lane == 0) mbar_arrive(bar + 8 * (C::bTFree + tile.i));  // read; see the barrier's count
+      tile.next();
     }
-    for (int c = (g & 1) ^ wg; c < x.nch; c += 2) {
-      const int G = g + c, st = G % C::NS, sb = G % C::NSB;
-      const int col = chunk<kDQ>(p, x, c).row;  // first column's query (or key, kDQ)
-      const int t0 = x.tile * kRows;
+    // rows of the chunks run through the window once (kDQ), or once per head
+    int at = kDQ ? 0 : (x.c0 + (G - g)) % x.nq;
+    for (; G < g + x.nch; G += kStep) {
+      int col = half;  // first column's query (or key, kDQ)
+      if (kDQ) {
+        const int c = G - g;
+        col += c < x.far ? c * C::kChunk : x.k0 + (c - x.far) * C::kChunk;
+      } else {
+        col += t0 + at * C::kChunk;
+        at += kStep;
+        while (at >= x.nq) at -= x.nq;
+      }
       bool whole;
       uint64_t mask = ~0ull;
       if (kDQ) {
-        whole = c >= x.far && col + kChunk - 1 <= t0 && col > t0 + kRows - 1 - p.window &&
+        whole = G - g >= x.far && col + 63 <= t0 && col > t0 + kRows - 1 - p.window &&
                 t0 + kRows <= x.L;
         if (!whole) {
           const int first = row >= p.window ? row - p.window + 1 : 0;
-          if (c < x.far) mask = bit_range(0, p.sinks - col);
+          if (G - g < x.far) mask = bit_range(0, p.sinks - col);
           else mask = bit_range(first - col, row + 1 - col) |
                       (x.far ? 0ull : bit_range(0, min(p.sinks, row + 1) - col));
           if (row >= x.L) mask = 0ull;
         }
       } else {
-        whole = col >= t0 + kRows - 1 && col - t0 < p.window - (kChunk - 1) &&
-                col + kChunk <= x.L;  // then the keys, which come before col, are below L too
+        whole = col >= t0 + kRows - 1 && col - t0 < p.window - 63 &&
+                col + 64 <= x.L;  // then the keys, which come before col, are below L too
         if (!whole) {
           const int64_t end = row < p.sinks ? x.L : static_cast<int64_t>(row) + p.window;
           mask = row < x.L ? bit_range(row - col, (end < x.L ? end : x.L) - col) : 0ull;
         }
       }
-      // the products of this group's previous chunk have read its P and dS (long since:
-      // waiting here keeps the wait's own cost out of the chain from S to P)
-      if (!all_ok(mbar_wait(bar + 8 * (C::bPFree + wg), ((G >> 1) & 1) ^ 1))) return kErrPFree;
-      if (!kDQ && !all_ok(mbar_wait(bar + 8 * (C::bCFull + st), (G / C::NS) & 1)))
-        return kErrGCFull;
-      if (!all_ok(mbar_wait(bar + 8 * (C::bSFull + wg), (G >> 1) & 1))) return kErrSFull;
+      // the products of an earlier chunk have read these P and dS (long since: waiting
+      // here keeps the wait's own cost out of the chain from S to P), and (kDQ not) the
+      // columns' statistics are there
+      bool ok = mbar_wait(bar + 8 * (C::bPFree + pb.i), pb.ph ^ 1);
+      if (!kDQ) ok = ok && mbar_wait(bar + 8 * (C::bCFull + ch.i), ch.ph);
+      if (!all_ok(ok && mbar_wait(sfull, full.ph))) return kErrSFull;
       tc_fence_after();
-      const float* nl = reinterpret_cast<const float*>(gbase + C::oCol + st * 2 * kChunk * 4);
-      const float* nd = nl + kChunk;
+      const float* nl = reinterpret_cast<const float*>(gbase + C::oCol + ch.i * 2 * C::kChunk * 4) + half;
+      const float* nd = nl + C::kChunk;
       const float2 sl = make_float2(sl2, sl2);
       float s[2][32], dp[2][32];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        tmem_ld32(trow + C::tS(sb) + 32 * j, s[j]);
-        tmem_ld32(trow + C::tS(sb) + kChunk + 32 * j, dp[j]);
+        tmem_ld32(trow + C::tS(sb.i) + half + 32 * j, s[j]);
+        tmem_ld32(trow + C::tS(sb.i) + C::kChunk + half + 32 * j, dp[j]);
       }
       tmem_wait_ld();
 #pragma unroll
@@ -602,7 +638,7 @@ __device__ int grad_warps(const Params& p, uint32_t base, uint8_t* gbase,
         reg_fence(dp[j]);
       }
       tc_fence_before();
-      mbar_arrive(bar + 8 * (C::bSFree + sb));
+      mbar_arrive(bar + 8 * (C::bSFree + sb.i));
 #pragma unroll
       for (int j = 0; j < 2; ++j) {  // 32 columns at a time
         uint32_t wp[16], ws[16];  // P and dS of columns 2 i, 2 i + 1
@@ -653,15 +689,18 @@ __device__ int grad_warps(const Params& p, uint32_t base, uint8_t* gbase,
 #pragma unroll
           for (int i = 0; i < 16; ++i) wp[i] = ws[i] = 0u;
         }
-        if (!kDQ) tmem_st16u(trow + C::tP(wg) + 16 * j, wp);
-        tmem_st16u(trow + C::tDS(wg) + 16 * j, ws);
+        if (!kDQ) tmem_st16u(trow + C::tP(pb.i) + half / 2 + 16 * j, wp);
+        tmem_st16u(trow + C::tDS(pb.i) + half / 2 + 16 * j, ws);
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(bar + 8 * (C::bPFull + wg));
+      mbar_arrive(bar + 8 * (C::bPFull + pb.i));
+      ch.next(kStep);
+      if (C::NSB > 1) sb.next(kStep);
+      if (C::kWide) pb.next(); else pb.ph ^= 1;
+      full.next();
     }
     g += x.nch;
-    ++tc;
   }
   return 0;
 }
@@ -775,10 +814,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar + 8 * (C::bCFull + i), 1);
       mbar_init(bar + 8 * (C::bCFree + i), 1);
     }
-    for (int i = 0; i < C::NSB; ++i) mbar_init(bar + 8 * (C::bSFree + i), 128);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar + 8 * (C::bSFull + i), 1);
-      mbar_init(bar + 8 * (C::bPFull + i), 128);
+    for (int i = 0; i < 2; ++i) mbar_init(bar + 8 * (C::bSFull + i), 1);
+    for (int i = 0; i < C::NSB; ++i) mbar_init(bar + 8 * (C::bSFree + i), C::kWide ? 256 : 128);
+    for (int i = 0; i < C::NPB; ++i) {
+      mbar_init(bar + 8 * (C::bPFull + i), C::kWide ? 256 : 128);
       mbar_init(bar + 8 * (C::bPFree + i), 1);
     }
     for (int i = 0; i < C::NACC; ++i) {
@@ -928,7 +967,7 @@ __global__ void __launch_bounds__(256) sink_join_kernel(const Params p, int tile
                          ? p.part0 + bh * parts * 2 * kRows * D
                          : p.part1 + (bh * (p.ntiles - 1) + tile - 1) * parts * 2 * kRows * D;
   src += (static_cast<int64_t>(out) * kRows + r) * D + c;
-  const int64_t all = static_cast<int64_t>(query_chunks(tile, L, p.window, p.sinks)) * p.group;
+  const int64_t all = static_cast<int64_t>(query_chunks(tile, L, p.window, p.sinks, chunk_rows(D, false))) * p.group;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i = 0; i < parts; ++i) {
     if (all * i / parts == all * (i + 1) / parts) continue;  // an empty part was not written
@@ -949,27 +988,30 @@ struct Plan {
 
 // Cuts key tiles into parts: the first ones when they are more than a third of an
 // SM's even share of all chunks (and larger than the others), the others when they
-// exceed that share; never below 16 chunks a part, which costs a tile of fp32
+// exceed that share; never below 1024 queries a part, which costs a tile of fp32
 // written and read.
 Plan make_plan(const SinkArgs& a) {
   Plan w;
   w.ntiles = (a.n + kRows - 1) / kRows;
   w.npad = w.ntiles * kRows;
   const int64_t group = a.heads / a.kv_heads, bkv = static_cast<int64_t>(a.batch) * a.kv_heads;
-  const int64_t c0 = group * query_chunks(0, a.n, a.window, a.sinks);
-  const int64_t c1 = w.ntiles > 1 ? group * query_chunks(1, a.n, a.window, a.sinks) : 0;
-  // tile t >= 1 has min(per, rest - 2 t) chunks a head: its window's, or to the sequence's end
-  const int64_t per = (static_cast<int64_t>(a.window) + kRows - 1 + kChunk - 1) / kChunk;
-  const int64_t rest = (static_cast<int64_t>(a.n) + kChunk - 1) / kChunk, last = w.ntiles - 1;
-  int64_t m = rest > per ? (rest - per) / 2 : 0;  // tiles 1..m have `per`
+  const int chunk = chunk_rows(a.d, false), f = kRows / chunk;  // f chunks span a tile
+  const int64_t c0 = group * query_chunks(0, a.n, a.window, a.sinks, chunk);
+  const int64_t c1 =
+      w.ntiles > 1 ? group * query_chunks(1, a.n, a.window, a.sinks, chunk) : 0;
+  // tile t >= 1 has min(per, rest - f t) chunks a head: its window's, or to the sequence's end
+  const int64_t per = (static_cast<int64_t>(a.window) + kRows - 1 + chunk - 1) / chunk;
+  const int64_t rest = (static_cast<int64_t>(a.n) + chunk - 1) / chunk, last = w.ntiles - 1;
+  int64_t m = rest > per ? (rest - per) / f : 0;  // tiles 1..m have `per`
   if (m > last) m = last;
-  const int64_t all =
-      c0 + group * (m * per + (last - m) * rest - (last * (last + 1) - m * (m + 1)));
+  const int64_t all = c0 + group * (m * per + (last - m) * rest -
+                                    f * (last * (last + 1) - m * (m + 1)) / 2);
   auto at_least = [](int64_t x, int64_t lo) { return x < lo ? lo : x; };
   const int64_t share = (all * bkv + 147) / 148;
-  const int64_t cap1 = at_least(share, 16);
+  const int64_t least = 1024 / chunk;  // chunks of a part, at least
+  const int64_t cap1 = at_least(share, least);
   const int64_t s1 = (c1 + cap1 - 1) / cap1;
-  const int64_t cap0 = at_least(share / 3, at_least(s1 > 1 ? cap1 : c1, 16));
+  const int64_t cap0 = at_least(share / 3, at_least(s1 > 1 ? cap1 : c1, least));
   const int64_t s0 = (c0 + cap0 - 1) / cap0;
   w.s0 = static_cast<int>(s0 < 1 ? 1 : s0);
   w.s1 = static_cast<int>(s1 < 1 ? 1 : s1);
@@ -993,14 +1035,14 @@ cudaError_t launch_main(const SinkArgs& a, Params p, cudaStream_t stream) {
   const bool maps =
       kDQ ? make_tmap_bf16_rows(&tx, a.q, D, a.n, hq, kRows) &&
                 make_tmap_bf16_rows(&ty, a.dout, D, a.n, hq, kRows) &&
-                make_tmap_bf16_rows(&cx, a.k, D, a.n, hk, kChunk) &&
-                make_tmap_bf16_rows(&cy, a.v, D, a.n, hk, kChunk) &&
+                make_tmap_bf16_rows(&cx, a.k, D, a.n, hk, C::kChunk) &&
+                make_tmap_bf16_rows(&cy, a.v, D, a.n, hk, C::kChunk) &&
                 make_tmap_bf16_rows(&to0, a.dq, D, a.n, hq, kRows) &&
                 make_tmap_bf16_rows(&to1, a.dq, D, a.n, hq, kRows)
           : make_tmap_bf16_rows(&tx, a.k, D, a.n, hk, kRows) &&
                 make_tmap_bf16_rows(&ty, a.v, D, a.n, hk, kRows) &&
-                make_tmap_bf16_rows(&cx, a.q, D, a.n, hq, kChunk) &&
-                make_tmap_bf16_rows(&cy, a.dout, D, a.n, hq, kChunk) &&
+                make_tmap_bf16_rows(&cx, a.q, D, a.n, hq, C::kChunk) &&
+                make_tmap_bf16_rows(&cy, a.dout, D, a.n, hq, C::kChunk) &&
                 make_tmap_bf16_rows(&to0, a.dv, D, a.n, hk, kRows) &&
                 make_tmap_bf16_rows(&to1, a.dk, D, a.n, hk, kRows);
   if (!maps) return cudaErrorInvalidValue;
