@@ -109,37 +109,47 @@ struct Cfg {
   static constexpr int kChunkSlab = kChunk * 128;  // swizzled box of a chunk
   // tiles that stay: two buffers at d = 64 (the next item's loads overlap), one at d = 128
   static constexpr int NT = D == 64 ? 2 : 1;
-  static constexpr int NS = D == 64 ? 6 : kWide ? 2 : 4;  // chunk stages
-  static constexpr int NSB = D == 64 && kDQ ? 2 : 1;      // S/dP buffers in tensor memory
-  static constexpr int NPB = 2;                           // P/dS buffers in tensor memory
-  static constexpr int NOUT = kDQ ? 1 : 2;                // gradients of an item
-  static constexpr int NACC = D == 64 ? 2 : 1;            // accumulator sets
+  // stages of the chunk's two operands X (Q, or K) and Y (dO, or V).  Wide: dQ needs V for
+  // dP only, so V's one stage is free long before K's and a third of K fits; V then has
+  // barriers and a producer of its own (two shared stages: 222 us where this takes 170, at
+  // 16 heads x 8192 x 128; at the other widths sharing barriers is 10-15 % faster).
+  static constexpr bool kSplit = kWide;
+  static constexpr int NX = D == 64 ? 6 : kWide ? 3 : 4;
+  static constexpr int NY = kSplit ? 1 : NX;
+  // buffers in tensor memory: S and dP, P and dS, accumulators
+  static constexpr int NSB = D == 64 && kDQ ? 2 : 1;
+  static constexpr int NPB = 2;
+  static constexpr int NOUT = kDQ ? 1 : 2;      // gradients of an item
+  static constexpr int NACC = D == 64 ? 2 : 1;
   static constexpr int kTile = kRows * D * 2;
-  static constexpr int kHalf = kChunk * D * 2;   // one of the chunk's two operands
-  static constexpr int oTile = 0;                // buffer i: X at oTile + 2 i kTile, Y after it
-  static constexpr int oCh = oTile + NT * 2 * kTile;  // stage s: X at oCh + 2 s kHalf, Y after it
-  static constexpr int oStg = oCh + NS * 2 * kHalf;   // output staging, 64 columns of a tile
-  static constexpr int oCol = oStg + kSlab;           // stage s: -lse log2 e and -D of its columns
+  static constexpr int kHalf = kChunk * D * 2;         // one operand of a chunk
+  static constexpr int oTile = 0;                      // buffer i: X at oTile + 2 i kTile, Y after it
+  static constexpr int oX = oTile + NT * 2 * kTile;
+  static constexpr int oY = oX + NX * kHalf;
+  static constexpr int oStg = oY + NY * kHalf;         // output staging, 64 columns of a tile
+  static constexpr int oCol = oStg + kSlab;            // X stage s: -lse log2 e and -D of its columns
   // kDQ: -lse log2 e and -D of the tile's rows, one set per tile buffer
-  static constexpr int oRow = oCol + (kDQ ? 0 : NS * 2 * kChunk * 4);
+  static constexpr int oRow = oCol + (kDQ ? 0 : NX * 2 * kChunk * 4);
   static constexpr int oItem = oRow + (kDQ ? NT * 2 * kRows * 4 : 0);  // ring of items
   static constexpr int oBar = oItem + kItems * 64;
-  static constexpr int bTFull = 0, bTFree = bTFull + NT, bCFull = bTFree + NT, bCFree = bCFull + NS,
-                       bSFull = bCFree + NS, bSFree = bSFull + 2, bPFull = bSFree + NSB,
-                       bPFree = bPFull + NPB, bAFull = bPFree + NPB, bAFree = bAFull + NACC, bIFull = bAFree + NACC,
-                       bIFree = bIFull + kItems, bFix = bIFree + kItems, bDone = bFix + 1, nBar = bDone + 1;
+  static constexpr int bTFull = 0, bTFree = bTFull + NT, bXFull = bTFree + NT, bXFree = bXFull + NX,
+                       bYFull = bXFree + NX, bYFree = bYFull + NY, bSFull = bYFree + NY,
+                       bSFree = bSFull + 2, bPFull = bSFree + NSB, bPFree = bPFull + NPB,
+                       bAFull = bPFree + NPB, bAFree = bAFull + NACC, bIFull = bAFree + NACC,
+                       bIFree = bIFull + kItems, bFix = bIFree + kItems, bDone = bFix + 2,
+                       nBar = bDone + 1;
   static constexpr int oSlot = oBar + nBar * 8;
   static constexpr int oPre = oSlot + 16;  // work table: pre[0..batch], len[0..batch)
   static constexpr int kSmem = oPre + (2 * kMaxBatch + 1) * 4 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
   static constexpr uint32_t kTmemCols = 512;
-  // accumulators first, then S and dP, then dS and P (two bf16 per column)
+  // accumulators first, then S, dP, then dS and P (two bf16 per column)
   __device__ static constexpr uint32_t tAcc(int acc, int out) { return (acc * NOUT + out) * D; }
-  static constexpr uint32_t tS0 = NACC * NOUT * D, tP0 = tS0 + NSB * 2 * kChunk;
-  __device__ static constexpr uint32_t tS(int sb) { return tS0 + sb * 2 * kChunk; }  // dP: + kChunk
-  __device__ static constexpr uint32_t tDS(int pb) { return tP0 + pb * NOUT * (kChunk / 2); }
+  __device__ static constexpr uint32_t tS(int sb) { return NACC * NOUT * D + sb * 2 * kChunk; }  // dP: + kChunk
+  __device__ static constexpr uint32_t tDS(int pb) { return tS(NSB) + pb * NOUT * (kChunk / 2); }
   __device__ static constexpr uint32_t tP(int pb) { return tDS(pb) + kChunk / 2; }
-  static_assert(tP0 + NPB * NOUT * (kChunk / 2) <= kTmemCols, "tensor memory columns");
+  static_assert(NACC * NOUT * D + NSB * 2 * kChunk + NPB * NOUT * (kChunk / 2) <= kTmemCols,
+                "tensor memory columns");
   static constexpr int kRegsCtl = 72;
   static constexpr int kRegsGrad = 176;
   static constexpr int kRegsEpi = 88;
@@ -296,10 +306,67 @@ __device__ __forceinline__ Chunk chunk(const Params& p, const Item& x, int c) {
   return k;
 }
 
-enum : int { kErrTFree = 0x81, kErrCFree, kErrFix, kErrTFull, kErrCFull, kErrSFree, kErrPFull,
-             kErrAFree, kErrSFull, kErrAFull, kErrDone, kErrIFree, kErrIFull, kErrGTFull };
+enum : int { kErrTFree = 0x81, kErrXFree, kErrFix, kErrTFull, kErrXFull, kErrSFree, kErrPFull, kErrAFree,
+             kErrSFull, kErrYFree, kErrYFull, kErrDone, kErrIFree, kErrIFull, kErrGTFull, kErrAFull };
 
-// Tiles and chunks (warp 0, the whole warp; lane 0 issues).
+// Position in a ring of N barriers and the parity of its current pass.
+template <int N>
+struct Ring {
+  int i = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int step = 1) {  // step <= N
+    i += step;
+    if (i >= N) {
+      i -= N;
+      ph ^= 1;
+    }
+  }
+};
+
+// A chunk's operands into their stages (whole warp; lane 0 issues): one, or where
+// map1 is not null two.  Where the chunk reaches past the length (other data lies
+// there: P is 0, but 0 x NaN is not) they land on `fixbar`, and the warp zeroes the
+// rows past the length before it hands the stage on.  `stats`: rows of statistics
+// that come along, or 0.
+template <int D, bool kDQ, bool kTwo>
+__device__ __forceinline__ int load_chunk(const Params& p, int L, Chunk k, uint32_t base,
+                                          uint8_t* gbase, const CUtensorMap* map0, int off0,
+                                          const CUtensorMap* map1, int off1, uint32_t full,
+                                          uint32_t fixbar, int& fixes, uint32_t stats, int lane) {
+  using C = Cfg<D, kDQ>;
+  const bool fix = k.row + C::kChunk > L && L < p.n;
+  const uint32_t land = fix ? fixbar : full;
+  if (lane == 0) {
+    mbar_arrive_expect_tx(land, (kTwo ? 2 : 1) * C::kHalf + (stats ? 2 * C::kChunk * 4 : 0));
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      tma_load_3d(base + off0 + i * C::kChunkSlab, map0, land, i * 64, k.row, k.bh);
+      if (kTwo) tma_load_3d(base + off1 + i * C::kChunkSlab, map1, land, i * 64, k.row, k.bh);
+    }
+    if (stats) {  // the columns' statistics, padded to whole tiles of 128
+      const int64_t at = static_cast<int64_t>(k.bh) * p.npad + k.row;
+      bulk_load(stats, p.nlse2 + at, C::kChunk * 4, land);
+      bulk_load(stats + C::kChunk * 4, p.nd + at, C::kChunk * 4, land);
+    }
+  }
+  if (!fix) return 0;
+  if (!__all_sync(0xffffffffu, mbar_wait(fixbar, fixes & 1))) return kErrFix;
+  ++fixes;
+#pragma unroll
+  for (int o = 0; o < (kTwo ? 2 : 1); ++o) {
+    uint4* v = reinterpret_cast<uint4*>(gbase + (o ? off1 : off0));
+    // whole 128-byte rows of every box, so the swizzle does not matter
+    for (int i = 0; i < D / 64; ++i)
+      for (int j = (L - k.row) * 8 + lane; j < C::kChunk * 8; j += 32)
+        v[i * (C::kChunkSlab / 16) + j] = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(full);
+  return 0;
+}
+
+// Items, tiles and the chunks' operands, kSplit: X alone (warp 0, the whole warp).
 template <int D, bool kDQ>
 __device__ int producer(const Params& p, const int* pre, uint32_t base, uint8_t* gbase, int lane,
                         const CUtensorMap* tx, const CUtensorMap* ty, const CUtensorMap* cx,
@@ -307,7 +374,8 @@ __device__ int producer(const Params& p, const int* pre, uint32_t base, uint8_t*
   using C = Cfg<D, kDQ>;
   const uint32_t bar = base + C::oBar;
   const int count = item_count<kDQ>(p, pre);
-  int g = 0, tc = 0, fixes = 0;
+  int tc = 0, fixes = 0;
+  Ring<C::NX> ring;
   int* taken = p.taken + (kDQ ? 1 : 0);
   int fetched = lane == 0 ? atomicAdd(taken, 1) : 0;
   for (int rd = 0;;) {
@@ -354,45 +422,43 @@ __device__ int producer(const Params& p, const int* pre, uint32_t base, uint8_t*
     }
     if (!__all_sync(0xffffffffu, ok)) return kErrTFree;
     for (int c = 0; c < x.nch; ++c) {
-      const int G = g + c, st = G % C::NS;
-      const Chunk k = chunk<D, kDQ>(p, x, c);
-      const bool fix = k.row + C::kChunk > x.L && x.L < p.n;  // rows past the length hold other data
-      const uint32_t full = bar + 8 * (C::bCFull + st);
-      const uint32_t land = fix ? bar + 8 * C::bFix : full;
-      const uint32_t s = base + C::oCh + st * 2 * C::kHalf;
-      if (lane == 0) {
-        ok = mbar_wait(bar + 8 * (C::bCFree + st), ((G / C::NS) & 1) ^ 1);
-        if (ok) {
-          mbar_arrive_expect_tx(land, 2 * C::kHalf + (kDQ ? 0 : 2 * C::kChunk * 4));
-#pragma unroll
-          for (int i = 0; i < D / 64; ++i) {
-            tma_load_3d(s + i * C::kChunkSlab, cx, land, i * 64, k.row, k.bh);
-            tma_load_3d(s + C::kHalf + i * C::kChunkSlab, cy, land, i * 64, k.row, k.bh);
-          }
-          if (!kDQ) {  // the columns' statistics, padded to whole tiles of 128
-            const int64_t at = static_cast<int64_t>(k.bh) * p.npad + k.row;
-            const uint32_t sc = base + C::oCol + st * 2 * C::kChunk * 4;
-            bulk_load(sc, p.nlse2 + at, C::kChunk * 4, land);
-            bulk_load(sc + C::kChunk * 4, p.nd + at, C::kChunk * 4, land);
-          }
-        }
-      }
-      if (!__all_sync(0xffffffffu, ok)) return kErrCFree;
-      if (fix) {
-        if (!__all_sync(0xffffffffu, mbar_wait(land, fixes & 1))) return kErrFix;
-        ++fixes;
-        uint4* v = reinterpret_cast<uint4*>(gbase + C::oCh + st * 2 * C::kHalf);
-        // whole 128-byte rows of every box, so the swizzle does not matter
-        for (int i = 0; i < 2 * (D / 64); ++i)
-          for (int j = (x.L - k.row) * 8 + lane; j < C::kChunk * 8; j += 32)
-            v[i * (C::kChunkSlab / 16) + j] = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full);
-      }
+      if (!__all_sync(0xffffffffu,
+                      lane != 0 || mbar_wait(bar + 8 * (C::bXFree + ring.i), ring.ph ^ 1)))
+        return kErrXFree;
+      const int err = load_chunk<D, kDQ, !C::kSplit>(
+          p, x.L, chunk<D, kDQ>(p, x, c), base, gbase, cx, C::oX + ring.i * C::kHalf, cy,
+          C::oY + ring.i * C::kHalf, bar + 8 * (C::bXFull + ring.i), bar + 8 * C::bFix, fixes,
+          kDQ ? 0 : base + C::oCol + ring.i * 2 * C::kChunk * 4, lane);
+      if (err) return err;
+      ring.next();
     }
-    g += x.nch;
     ++tc;
+  }
+  return 0;
+}
+
+// kSplit: the Y operand of the chunks (warp 3, the whole warp).
+template <int D, bool kDQ>
+__device__ int y_producer(const Params& p, uint32_t base, uint8_t* gbase, int lane,
+                          const CUtensorMap* cy) {
+  using C = Cfg<D, kDQ>;
+  const uint32_t bar = base + C::oBar;
+  int fixes = 0;
+  Ring<C::NY> ring;
+  for (int rd = 0;; ++rd) {
+    Item x;
+    if (!next_item<D, kDQ>(x, rd, bar, gbase, lane)) return kErrIFull;
+    if (x.nch < 0) break;
+    for (int c = 0; c < x.nch; ++c) {
+      if (!__all_sync(0xffffffffu,
+                      lane != 0 || mbar_wait(bar + 8 * (C::bYFree + ring.i), ring.ph ^ 1)))
+        return kErrYFree;
+      const int err = load_chunk<D, kDQ, false>(
+          p, x.L, chunk<D, kDQ>(p, x, c), base, gbase, cy, C::oY + ring.i * C::kHalf, nullptr, 0,
+          bar + 8 * (C::bYFull + ring.i), bar + 8 * (C::bFix + 1), fixes, 0, lane);
+      if (err) return err;
+      ring.next();
+    }
   }
   return 0;
 }
@@ -410,42 +476,21 @@ __device__ __forceinline__ int next_chunks(int rd, uint32_t bar, const uint8_t* 
   return nch;
 }
 
-// Position in a ring of N barriers and the parity of its current pass.
-template <int N>
-struct Ring {
-  int i = 0;
-  uint32_t ph = 0;
-  __device__ __forceinline__ void next(int step = 1) {  // step <= N
-    i += step;
-    if (i >= N) {
-      i -= N;
-      ph ^= 1;
-    }
-  }
-};
-
-// Waits for two barriers, asking for both before looking at either answer.
-__device__ __forceinline__ int wait_both(uint32_t bar0, uint32_t ph0, uint32_t bar1, uint32_t ph1) {
-  const bool ok0 = mbar_try_wait(bar0, ph0), ok1 = mbar_try_wait(bar1, ph1);
-  if (!ok0 && !mbar_wait(bar0, ph0)) return 1;
-  if (!ok1 && !mbar_wait(bar1, ph1)) return 2;
-  return 0;
-}
-
 // S and dP of every chunk (warp 1, one thread).  A lone thread takes four cycles
 // and more an instruction, and what it does between two chunks is time the tensor
-// cores stand still: positions advance by steps, descriptors by adds.
+// cores may stand still: positions advance by steps, descriptors by adds.
 template <int D, bool kDQ>
 __device__ int s_issuer(const Params& p, uint32_t base, const uint8_t* gbase, uint32_t tmem) {
   using C = Cfg<D, kDQ>;
   const uint32_t bar = base + C::oBar;
   constexpr uint32_t kId = idesc_bf16_f32(128, C::kChunk, false, false);
-  const uint64_t dX0 = smem_desc_sw128(base + C::oTile, 0, 1024);
-  const uint64_t dY0 = smem_desc_sw128(base + C::oTile + C::kTile, 0, 1024);
-  const uint64_t eX0 = smem_desc_sw128(base + C::oCh, 0, 1024);
-  const uint64_t eY0 = smem_desc_sw128(base + C::oCh + C::kHalf, 0, 1024);
+  const uint64_t tX = smem_desc_sw128(base + C::oTile, 0, 1024);
+  const uint64_t tY = smem_desc_sw128(base + C::oTile + C::kTile, 0, 1024);
+  const uint64_t cX = smem_desc_sw128(base + C::oX, 0, 1024);
+  const uint64_t cY = smem_desc_sw128(base + C::oY, 0, 1024);
   Ring<C::NT> tile;
-  Ring<C::NS> ch;
+  Ring<C::NX> xr;
+  Ring<C::NY> yr;
   Ring<C::NSB> sb;
   int G = 0;
   for (int rd = 0;; ++rd) {
@@ -453,15 +498,19 @@ __device__ int s_issuer(const Params& p, uint32_t base, const uint8_t* gbase, ui
     if (nch == kNoItem) return kErrIFull;
     if (nch < 0) break;
     const uint32_t ot = tile.i * (2 * C::kTile >> 4);
+    const uint64_t dX = desc_add(tX, ot), dY = desc_add(tY, ot);
     if (!mbar_wait(bar + 8 * (C::bTFull + tile.i), tile.ph)) return kErrTFull;
     for (int c = 0; c < nch; ++c, ++G) {
-      const uint32_t oc = ch.i * (2 * C::kHalf >> 4);
-      const uint64_t dX = desc_add(dX0, ot), dY = desc_add(dY0, ot);
-      const uint64_t eX = desc_add(eX0, oc), eY = desc_add(eY0, oc);
-      const int late = wait_both(bar + 8 * (C::bCFull + ch.i), ch.ph,
-                                 bar + 8 * (C::bSFree + sb.i), sb.ph ^ 1);
-      if (late) return late == 1 ? kErrCFull : kErrSFree;
+      // the chunk is there, and the scores that used the buffers before have moved to
+      // registers; all are asked for before the first answer is looked at
+      const uint32_t xbar = bar + 8 * (C::bXFull + xr.i), ybar = bar + 8 * (C::bYFull + yr.i);
+      const uint32_t sfree = bar + 8 * (C::bSFree + sb.i);
+      const bool okx = mbar_try_wait(xbar, xr.ph), oks = mbar_try_wait(sfree, sb.ph ^ 1);
+      const bool oky = !C::kSplit || mbar_try_wait(ybar, yr.ph);
+      if (!okx && !mbar_wait(xbar, xr.ph)) return kErrXFull;
+      if (!oks && !mbar_wait(sfree, sb.ph ^ 1)) return kErrSFree;
       tc_fence_after();
+      const uint64_t eX = desc_add(cX, xr.i * (C::kHalf >> 4));
       const uint32_t tS = tmem + C::tS(sb.i), tDP = tS + C::kChunk;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
@@ -469,6 +518,11 @@ __device__ int s_issuer(const Params& p, uint32_t base, const uint8_t* gbase, ui
         const uint32_t kc = ((k >> 2) * C::kChunkSlab + (k & 3) * 32) >> 4;
         mma_bf16_ss(tS, desc_add(dX, kt), desc_add(eX, kc), kId, k > 0);
       }
+      if (C::kSplit) {
+        if (!oky && !mbar_wait(ybar, yr.ph)) return kErrYFull;
+        tc_fence_after();
+      }
+      const uint64_t eY = desc_add(cY, yr.i * (C::kHalf >> 4));
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint32_t kt = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
@@ -477,8 +531,10 @@ __device__ int s_issuer(const Params& p, uint32_t base, const uint8_t* gbase, ui
       }
       // groups that take turns have a barrier each, so that each sees all its phases
       mma_commit(bar + 8 * (C::bSFull + (C::kWide ? 0 : G & 1)));
+      if (C::kSplit) mma_commit(bar + 8 * (C::bYFree + yr.i));  // V's only reader
       if (c == nch - 1) mma_commit(bar + 8 * (C::bTFree + tile.i));  // the tile's only readers
-      ch.next();
+      xr.next();
+      yr.next();
       sb.next();
     }
     tile.next();
@@ -494,10 +550,11 @@ __device__ int grad_issuer(const Params& p, uint32_t base, const uint8_t* gbase,
   using C = Cfg<D, kDQ>;
   const uint32_t bar = base + C::oBar;
   constexpr uint32_t kId = idesc_bf16_f32(128, D, false, true);
-  const uint64_t eX0 = smem_desc_sw128(base + C::oCh, C::kChunkSlab, 1024);
-  const uint64_t eY0 = smem_desc_sw128(base + C::oCh + C::kHalf, C::kChunkSlab, 1024);
+  const uint64_t cX = smem_desc_sw128(base + C::oX, C::kChunkSlab, 1024);
+  const uint64_t cY = smem_desc_sw128(base + C::oY, C::kChunkSlab, 1024);
   Ring<C::NACC> acc;
-  Ring<C::NS> ch;
+  Ring<C::NX> xr;
+  Ring<C::NY> yr;
   Ring<C::NPB> pb;
   for (int rd = 0;; ++rd) {
     const int nch = next_chunks<D, kDQ>(rd, bar, gbase);
@@ -506,8 +563,7 @@ __device__ int grad_issuer(const Params& p, uint32_t base, const uint8_t* gbase,
     const uint32_t out0 = tmem + C::tAcc(acc.i, 0);
     if (!mbar_wait(bar + 8 * (C::bAFree + acc.i), acc.ph ^ 1)) return kErrAFree;
     for (int c = 0; c < nch; ++c) {
-      const uint32_t oc = ch.i * (2 * C::kHalf >> 4);
-      const uint64_t eX = desc_add(eX0, oc), eY = desc_add(eY0, oc);
+      const uint64_t eX = desc_add(cX, xr.i * (C::kHalf >> 4));
       const uint32_t tP = tmem + C::tP(pb.i), tDS = tmem + C::tDS(pb.i);
       if (!mbar_wait(bar + 8 * (C::bPFull + pb.i), pb.ph)) return kErrPFull;
       tc_fence_after();
@@ -517,6 +573,7 @@ __device__ int grad_issuer(const Params& p, uint32_t base, const uint8_t* gbase,
           mma_bf16_ts(out0, tDS + 8 * k, desc_add(eX, (k * 2048) >> 4), kId, c > 0 || k > 0);
       } else {    // dV += P^T dO, dK += dS^T Q
         const uint32_t out1 = tmem + C::tAcc(acc.i, C::NOUT - 1);
+        const uint64_t eY = desc_add(cY, yr.i * (C::kHalf >> 4));
 #pragma unroll
         for (int k = 0; k < C::kChunk / 16; ++k)
           mma_bf16_ts(out0, tP + 8 * k, desc_add(eY, (k * 2048) >> 4), kId, c > 0 || k > 0);
@@ -525,9 +582,10 @@ __device__ int grad_issuer(const Params& p, uint32_t base, const uint8_t* gbase,
           mma_bf16_ts(out1, tDS + 8 * k, desc_add(eX, (k * 2048) >> 4), kId, c > 0 || k > 0);
       }
       mma_commit(bar + 8 * (C::bPFree + pb.i));
-      mma_commit(bar + 8 * (C::bCFree + ch.i));
+      mma_commit(bar + 8 * (C::bXFree + xr.i));
       if (c == nch - 1) mma_commit(bar + 8 * (C::bAFull + acc.i));
-      ch.next();
+      xr.next();
+      yr.next();
       pb.next();
     }
     acc.next();
@@ -556,12 +614,12 @@ __device__ int grad_warps(const Params& p, uint32_t base, uint8_t* gbase,
   // this group's chunks: all (wide), or those of its parity, counted over all items
   constexpr int kStep = C::kWide ? 1 : 2;
   int G = C::kWide ? 0 : wg, g = 0;  // its next chunk, and the item's first
-  Ring<C::NS> ch;                    // chunk G's stage, S/dP buffer, P/dS buffer; the
+  Ring<C::NX> xr;                    // chunk G's X stage, S/dP buffer, P/dS buffer; the
   Ring<C::NSB> sb;                   // parity of its own S barrier is full.ph
   Ring<C::NPB> pb;
   Ring<1> full;
   if (!C::kWide && wg) {
-    ch.next();
+    xr.next();
     sb.next();
     pb.next();
   }
@@ -619,10 +677,10 @@ __device__ int grad_warps(const Params& p, uint32_t base, uint8_t* gbase,
       // here keeps the wait's own cost out of the chain from S to P), and (kDQ not) the
       // columns' statistics are there
       bool ok = mbar_wait(bar + 8 * (C::bPFree + pb.i), pb.ph ^ 1);
-      if (!kDQ) ok = ok && mbar_wait(bar + 8 * (C::bCFull + ch.i), ch.ph);
+      if (!kDQ) ok = ok && mbar_wait(bar + 8 * (C::bXFull + xr.i), xr.ph);
       if (!all_ok(ok && mbar_wait(sfull, full.ph))) return kErrSFull;
       tc_fence_after();
-      const float* nl = reinterpret_cast<const float*>(gbase + C::oCol + ch.i * 2 * C::kChunk * 4) + half;
+      const float* nl = reinterpret_cast<const float*>(gbase + C::oCol + xr.i * 2 * C::kChunk * 4) + half;
       const float* nd = nl + C::kChunk;
       const float2 sl = make_float2(sl2, sl2);
       float s[2][32], dp[2][32];
@@ -695,7 +753,7 @@ __device__ int grad_warps(const Params& p, uint32_t base, uint8_t* gbase,
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(bar + 8 * (C::bPFull + pb.i));
-      ch.next(kStep);
+      xr.next(kStep);
       if (C::NSB > 1) sb.next(kStep);
       if (C::kWide) pb.next(); else pb.ph ^= 1;
       full.next();
@@ -810,11 +868,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the issuer's commit, and (kDQ) the eight warps that have read the row statistics
       mbar_init(bar + 8 * (C::bTFree + i), kDQ ? 9 : 1);
     }
-    for (int i = 0; i < C::NS; ++i) {
-      mbar_init(bar + 8 * (C::bCFull + i), 1);
-      mbar_init(bar + 8 * (C::bCFree + i), 1);
+    for (int i = 0; i < C::NX; ++i) {
+      mbar_init(bar + 8 * (C::bXFull + i), 1);
+      mbar_init(bar + 8 * (C::bXFree + i), 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(bar + 8 * (C::bSFull + i), 1);
+    for (int i = 0; i < C::NY; ++i) {
+      mbar_init(bar + 8 * (C::bYFull + i), 1);
+      mbar_init(bar + 8 * (C::bYFree + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar + 8 * (C::bSFull + i), 1);
+      mbar_init(bar + 8 * (C::bFix + i), 1);
+    }
     for (int i = 0; i < C::NSB; ++i) mbar_init(bar + 8 * (C::bSFree + i), C::kWide ? 256 : 128);
     for (int i = 0; i < C::NPB; ++i) {
       mbar_init(bar + 8 * (C::bPFull + i), C::kWide ? 256 : 128);
@@ -826,9 +891,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(bar + 8 * (C::bIFull + i), 1);
-      mbar_init(bar + 8 * (C::bIFree + i), kTakers);
+      mbar_init(bar + 8 * (C::bIFree + i), kTakers + (C::kSplit ? 1 : 0));
     }
-    mbar_init(bar + 8 * C::bFix, 1);
     mbar_init(bar + 8 * C::bDone, 2);  // one commit per MMA-issuing thread
     fence_barrier_init();
   }
@@ -858,6 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) err = producer<D, kDQ>(p, pre, base, gbase, lane, &tx, &ty, &cx, &cy);
     if (warp == 1 && lane == 0) err = s_issuer<D, kDQ>(p, base, gbase, tmem);
     if (warp == 2 && lane == 0) err = grad_issuer<D, kDQ>(p, base, gbase, tmem);
+    if (C::kSplit && warp == 3) err = y_producer<D, kDQ>(p, base, gbase, lane, &cy);
   } else if (warp < 12) {
     regs_inc<C::kRegsGrad, kLaunchRegs>();
     err = grad_warps<D, kDQ>(p, base, gbase, tmem, (warp - 4) >> 2, warp & 3, lane);
