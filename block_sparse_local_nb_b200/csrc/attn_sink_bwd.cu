@@ -80,7 +80,7 @@ struct Params {
 };
 
 __device__ __forceinline__ int length_of(const Params& p, int b) {
-  const int L = p.lengths ? p.lengths[b] : p.n;
+  const int L = p.lengths ? __ldcg(p.lengths + b) : p.n;
   return min(max(L, 0), p.n);
 }
 
@@ -908,13 +908,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(base + C::oSlot, C::kTmemCols);
     tmem_relinquish();
   }
-  pdl_wait();  // everything above overlaps the previous kernel's tail
+  // Everything above overlaps the previous kernel's tail.  The dQ kernel needs the row
+  // statistics and nothing of the dK/dV kernel before it, whose blocks allow its launch only
+  // once all their threads have seen the row kernel complete: so dQ blocks start as SMs run
+  // out of key tiles, and wait for that kernel at their own end, for those behind them.
+  if (!kDQ) pdl_wait();
   int* pre = reinterpret_cast<int*>(gbase + C::oPre);
   if (warp == 0) build_table<kDQ>(pre, p, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + C::oSlot);
+  if (!kDQ) pdl_trigger();
 
   int err = 0;
   if (warp < 4) {
@@ -932,7 +937,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (err) record_error(p.err, err);
 
-  pdl_trigger();
+  if (kDQ) {
+    pdl_trigger();
+    pdl_wait();
+  }
   __syncthreads();
   if (warp == 2 && lane == 0) mma_commit(bar + 8 * C::bDone);
   if (warp == 1) {
