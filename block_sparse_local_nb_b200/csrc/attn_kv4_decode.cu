@@ -105,41 +105,36 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         "f"(c[2]), "f"(c[3]));
 }
 
-// (x & mask) | magic in one instruction: the operands come in registers, since an
-// instruction takes one immediate only.
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t magic) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(mask), "r"(magic));
-  return r;
+// A nibble alone in a bf16 is a number: the least significant bit of the exponent
+// goes on where the mantissa of the subnormals ends, so c in bits 0-3 is c 2^-133 and
+// c in bits 4-7 is c 2^-129, exactly.  One `and` yields a pair of codes of two halves.
+__device__ __forceinline__ uint32_t even_codes(uint32_t w) { return w & 0x000f000fu; }
+__device__ __forceinline__ uint32_t odd_codes(uint32_t w) { return w & 0x00f000f0u; }
+
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {  // two bf16 products
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
-struct Magic {
-  uint32_t kmask, kbase;  // nibbles at bit 0 of both halves; 128 as bf16
-  uint32_t vmask, vbase;  // nibbles at bit 2; 32
-  uint32_t centre;        // 39.5
-};
-// Values that the compiler cannot fold back into immediates.
-__device__ __forceinline__ Magic make_magic() {
-  Magic m;
-  asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(m.kmask));
-  asm volatile("mov.b32 %0, 0x43004300;" : "=r"(m.kbase));
-  asm volatile("mov.b32 %0, 0x003c003c;" : "=r"(m.vmask));
-  asm volatile("mov.b32 %0, 0x42004200;" : "=r"(m.vbase));
-  asm volatile("mov.b32 %0, 0x421e421e;" : "=r"(m.centre));
-  return m;
+// The codes times 2^127 less their centre: (c - 7.5) / 64 of the even ones, (c - 7.5) / 4
+// of the odd ones, exact.
+constexpr float kEvenUnit = 64.f, kOddUnit = 4.f;
+__device__ __forceinline__ uint32_t centred(uint32_t codes, uint32_t centre) {
+  const uint32_t up = 0x7f007f00u;
+  const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&codes),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&up),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&centre));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t centred_even(uint32_t w) {
+  return centred(even_codes(w), 0xbdf0bdf0u);  // -7.5 / 64
+}
+__device__ __forceinline__ uint32_t centred_odd(uint32_t w) {
+  return centred(odd_codes(w), 0xbff0bff0u);  // -7.5 / 4
 }
 
-// Nibbles i and i + 4 of w as the bf16 pair (128 + c_i, 128 + c_{i+4}).
-template <int I>
-__device__ __forceinline__ uint32_t codes_bf16(const Magic& m, uint32_t w) {
-  return and_or(w >> (4 * I), m.kmask, m.kbase);
-}
-// (c_i - 7.5, c_{i+4} - 7.5): 32 + c (the nibble two bits up) minus 39.5, exact
-template <int I>
-__device__ __forceinline__ uint32_t centred_bf16(const Magic& m, uint32_t w) {
-  const uint32_t x = and_or(I == 0 ? w << 2 : w >> (4 * I - 2), m.vmask, m.vbase);
-  __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x),
-                             *reinterpret_cast<const __nv_bfloat162*>(&m.centre));
-  return *reinterpret_cast<uint32_t*>(&r);
+__device__ __forceinline__ float pow2(int e) {  // -126 <= e <= 127
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
 __device__ __forceinline__ float step_of(uint32_t par) { return __uint_as_float(par << 16); }
@@ -265,34 +260,61 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
 
   // query operand: k-step 2 g + i of the products holds channels 32 g + 8 t + 2 i
   // + {0, 4} (first half) and {1, 5} (second half) of lane t, matching the nibble
-  // pairs of a code word.  off_g = -135.5 sum(q_g) of heads 2 t, 2 t + 1.
+  // pairs of a code word.  With 2^e the largest power of two in the head's row, the
+  // operands are q 2^(126 - e) for the even codes (c 2^-133) and a sixteenth of it for
+  // the odd ones (c 2^-129): the products are q c 2^(-7 - e), and the scores carry that
+  // factor until sl2 takes it out.  off_g = -7.5 sum(q_g) of heads 2 t, 2 t + 1.
   constexpr int NP = NG / 2;
   uint32_t qb[kSets][2 * NG][2], qm[kSets][2];
-  float off[kSets][NG][2];
+  float off[kSets][NG][2], sl2[kSets][2];
 #pragma unroll
   for (int hs = 0; hs < kSets; ++hs) {
     const int head = r + 8 * hs;
     const bool in = head < nh;
     const uint4* src = reinterpret_cast<const uint4*>(
         p.q + (static_cast<int64_t>(b) * p.heads + head0 + (in ? head : 0)) * D);
+    uint4 x[NG];
+    uint32_t top = 0;  // the largest magnitude: bf16 bits order like integers
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      x[g] = in ? src[4 * g + t] : make_uint4(0, 0, 0, 0);  // channels 32 g + 8 t ..+ 7
+      const uint32_t w[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+    }
+    top = max(top & 0xffffu, top >> 16);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // subnormal rows count as 2^-126, infinite ones as 2^127 (their scores are no numbers)
+    const int e = min(max(static_cast<int>(top >> 7), 1), 254) - 127;
+    const uint32_t down1 = e == 127 ? 0x0040u : static_cast<uint32_t>(127 - e) << 7;  // 2^-e
+    const uint32_t down = down1 | down1 << 16;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int n = 7 + __shfl_sync(0xffffffffu, e, 8 * t + 4 * j);
+      // beyond the largest float no two different scores have comparable weights
+      sl2[hs][j] = fminf(p.sl2 * pow2(n / 2) * pow2(n - n / 2), 3.402823466e38f);
+    }
     float qs[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const uint4 x = in ? src[4 * g + t] : make_uint4(0, 0, 0, 0);  // channels 32 g + 8 t ..+ 7
-      qb[hs][2 * g][0] = __byte_perm(x.x, x.z, 0x5410);      // 0, 4
-      qb[hs][2 * g][1] = __byte_perm(x.x, x.z, 0x7632);      // 1, 5
-      qb[hs][2 * g + 1][0] = __byte_perm(x.y, x.w, 0x5410);  // 2, 6
-      qb[hs][2 * g + 1][1] = __byte_perm(x.y, x.w, 0x7632);  // 3, 7
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      const uint32_t w[4] = {mul2(x[g].x, down), mul2(x[g].y, down), mul2(x[g].z, down),
+                             mul2(x[g].w, down)};  // below 2
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         sum += __uint_as_float(w[i] << 16) + __uint_as_float(w[i] & 0xffff0000u);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // 0, 4 and 1, 5; then 2, 6 and 3, 7
+        qb[hs][2 * g + i][0] = mul2(__byte_perm(w[i], w[i + 2], 0x5410), 0x7e807e80u);  // 2^126
+        qb[hs][2 * g + i][1] = mul2(__byte_perm(w[i], w[i + 2], 0x7632), 0x7c807c80u);  // 2^122
+      }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      sum *= 0.0078125f;
       qs[g] = sum;
-      off[hs][g][0] = -135.5f * __shfl_sync(0xffffffffu, sum, 8 * t);
-      off[hs][g][1] = -135.5f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+      off[hs][g][0] = -7.5f * __shfl_sync(0xffffffffu, sum, 8 * t);
+      off[hs][g][1] = -7.5f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
     }
     // lane t of the midpoint product multiplies the pair (m_2u, m_2u+1), u = t mod
     // NP, by part t / NP of the sums (and by one part more in its second half)
@@ -327,7 +349,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
       for (int e = 0; e < 4; ++e) o[hs][i][e] = 0.f;
   }
 
-  const Magic mg = make_magic();
   // One page; kWhole: every token of it is visible (all but the edge pages), which
   // keeps the common path free of branches.
   auto page = [&](const uint8_t* pg, int tok0, auto whole_tag) {
@@ -355,10 +376,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
         mma16816(s[hs][mt], ma, qm[hs][0], qm[hs][1], zero);  // sum_g m_g sum(q_g)
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        const uint32_t a0[4] = {codes_bf16<0>(mg, w[0][g]), codes_bf16<0>(mg, w[1][g]),
-                                codes_bf16<1>(mg, w[0][g]), codes_bf16<1>(mg, w[1][g])};
-        const uint32_t a1[4] = {codes_bf16<2>(mg, w[0][g]), codes_bf16<2>(mg, w[1][g]),
-                                codes_bf16<3>(mg, w[0][g]), codes_bf16<3>(mg, w[1][g])};
+        const uint32_t h0 = w[0][g] >> 8, h1 = w[1][g] >> 8;
+        const uint32_t a0[4] = {even_codes(w[0][g]), even_codes(w[1][g]), odd_codes(w[0][g]),
+                                odd_codes(w[1][g])};
+        const uint32_t a1[4] = {even_codes(h0), even_codes(h1), odd_codes(h0), odd_codes(h1)};
         const float st0 = step_of(par[0][g]), st1 = step_of(par[1][g]);
 #pragma unroll
         for (int hs = 0; hs < kSets; ++hs) {
@@ -387,15 +408,16 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
     for (int hs = 0; hs < kSets; ++hs) {
       float mx[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        mx[j] = fmaxf(fmaxf(s[hs][0][j], s[hs][0][2 + j]), fmaxf(s[hs][1][j], s[hs][1][2 + j]));
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1)
-          mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], x));
-        mx[j] *= p.sl2;
-      }
+      for (int j = 0; j < 2; ++j)
+        mx[j] = sl2[hs][j] *
+                fmaxf(fmaxf(s[hs][0][j], s[hs][0][2 + j]), fmaxf(s[hs][1][j], s[hs][1][2 + j]));
       // the maximum in use may lag by 2^8: exact after the final division
       if (__any_sync(0xffffffffu, mx[0] > m[hs][0] + kTau || mx[1] > m[hs][1] + kTau)) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1)  // over the lanes that hold the page's other tokens
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], x));
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float mn = fmaxf(m[hs][j], mx[j]);
@@ -417,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float& x = s[hs][i >> 1][2 * (i & 1) + j];
-          x = ex2_approx(fmaf(x, p.sl2, nm));
+          x = ex2_approx(fmaf(x, sl2[hs][j], nm));
           l[hs][j] += x;
         }
       }
@@ -459,10 +481,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
           const uint32_t sel = half ? 0x7632u : 0x5410u;
           const uint32_t x = __byte_perm(vw[0][w], vw[1][w], sel);
           const uint32_t y = __byte_perm(vw[2][w], vw[3][w], sel);
-          const uint32_t a0[4] = {centred_bf16<0>(mg, x), centred_bf16<1>(mg, x),
-                                  centred_bf16<0>(mg, y), centred_bf16<1>(mg, y)};
-          const uint32_t a1[4] = {centred_bf16<2>(mg, x), centred_bf16<3>(mg, x),
-                                  centred_bf16<2>(mg, y), centred_bf16<3>(mg, y)};
+          const uint32_t x8 = x >> 8, y8 = y >> 8;
+          const uint32_t a0[4] = {centred_even(x), centred_odd(x), centred_even(y), centred_odd(y)};
+          const uint32_t a1[4] = {centred_even(x8), centred_odd(x8), centred_even(y8),
+                                  centred_odd(y8)};
           const int g = 2 * w + half;
 #pragma unroll
           for (int hs = 0; hs < kSets; ++hs) {
@@ -527,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
       float* dst = join + at * C::kJoinRow + r;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
-        dst[16 * c] = o[hs][c][j];
-        dst[16 * c + 8] = o[hs][c][2 + j];
+        dst[16 * c] = kEvenUnit * o[hs][c][j];
+        dst[16 * c + 8] = kOddUnit * o[hs][c][2 + j];
       }
     }
   }
