@@ -47,7 +47,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 template <int D>
 struct Cfg {
   using P = Page<D>;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = D == 64 ? 3 : 4;
   static constexpr int kRing = kWarps * kStages * P::kBytes;
   // the warps' results take the place of the ring when the pages are done
   // (rows of D + 4 floats: the lanes of a store fall into different banks)
@@ -192,8 +192,12 @@ __device__ __forceinline__ void store_row(const Params& p, int d, int64_t row, i
   if (c == 0 && p.lse) p.lse[row] = has ? (mx + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-// Blocks that should fit an SM at once (registers; the shared memory follows).
-constexpr int blocks_per_sm(int d, int sets) { return d == 64 ? (sets == 1 ? 4 : 3) : (sets == 1 ? 3 : 2); }
+// Blocks that should fit an SM at once (registers; the shared memory follows).  At
+// d = 128 two blocks of 200 registers schedule better than three of 168: 57 us against
+// 62 at 32 ragged contexts of up to 8192 tokens, 45 either way at one of 2^20; four of
+// 128 take 79 and 58.  At d = 64 five blocks of 96 take 22.3 us where four take 18.5
+// (64 streams x 4100 visible tokens), and three 18.5.
+constexpr int blocks_per_sm(int d, int sets) { return d == 64 ? (sets == 1 ? 4 : 3) : 2; }
 
 // kSets: sets of eight heads (the columns of a product): 1 when at most eight
 // share the cache, 2 otherwise.
@@ -694,7 +698,7 @@ struct Plan {
 Plan plan_for(const Kv4DecodeArgs& a) {
   const int64_t blocks =
       static_cast<int64_t>(a.batch) * a.kv_heads * ceil_div(a.heads / a.kv_heads, kHeads);
-  const int64_t want = ceil_div(148 * 3, blocks);
+  const int64_t want = ceil_div(148 * (a.d == 64 ? 3 : 2), blocks);
   const int64_t most = ceil_div(most_pages(a), kMinShare);
   int64_t s = want < most ? want : most;
   if (s < 1) s = 1;
