@@ -413,18 +413,19 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
       float mx[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        mx[j] = sl2[hs][j] *
-                fmaxf(fmaxf(s[hs][0][j], s[hs][0][2 + j]), fmaxf(s[hs][1][j], s[hs][1][2 + j]));
-      // the maximum in use may lag by 2^8: exact after the final division
-      if (__any_sync(0xffffffffu, mx[0] > m[hs][0] + kTau || mx[1] > m[hs][1] + kTau)) {
+        mx[j] = sl2[hs][j] * max_nan(max_nan(s[hs][0][j], s[hs][0][2 + j]),
+                                     max_nan(s[hs][1][j], s[hs][1][2 + j]));
+      // the maximum in use may lag by 2^8: exact after the final division.  A score that
+      // is no number becomes the maximum, and the output then is none either.
+      if (__any_sync(0xffffffffu, !(mx[0] <= m[hs][0] + kTau && mx[1] <= m[hs][1] + kTau))) {
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1)  // over the lanes that hold the page's other tokens
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], x));
+            mx[j] = max_nan(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], x));
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float mn = fmaxf(m[hs][j], mx[j]);
+          const float mn = max_nan(m[hs][j], mx[j]);
           const float a = m[hs][j] == -INFINITY ? 0.f : ex2_approx(m[hs][j] - mn);
           m[hs][j] = mn;
           l[hs][j] *= a;
@@ -563,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
     const int head = idx / (D / 2), c = idx % (D / 2);
     float mx = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, join_ml[w * kHeads + head].x);
+    for (int w = 0; w < kWarps; ++w) mx = max_nan(mx, join_ml[w * kHeads + head].x);
     float sum = 0.f;
     float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
@@ -605,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
       if (i < p.splits) {
         ml[i] = load_cluster(at_ml, i);
         x[i] = load_cluster(at, i);
-        mx = fmaxf(mx, ml[i].x);
+        mx = max_nan(mx, ml[i].x);
       }
     float sum = 0.f;
     float2 acc = make_float2(0.f, 0.f);
@@ -638,13 +639,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(const Params 
   const float4* part =
       reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(row) * p.splits * D) + c;
   float mx = -INFINITY;
-  for (int s = threadIdx.x; s < p.splits; s += 32 * kJoinWarps) mx = fmaxf(mx, ml[s].x);
+  for (int s = threadIdx.x; s < p.splits; s += 32 * kJoinWarps) mx = max_nan(mx, ml[s].x);
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+  for (int x = 16; x > 0; x >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, x));
   if (lane == 0) max_s[warp] = mx;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, max_s[w]);
+  for (int w = 0; w < kJoinWarps; ++w) mx = max_nan(mx, max_s[w]);
   const bool has = mx != -INFINITY;  // some share saw a token
   float sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -33,17 +33,6 @@ using namespace kv4;
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // The largest bf16 <= x (x finite or NaN; NaN stays NaN), as a float.
 __device__ __forceinline__ float bf16_below(float x) {
   const uint32_t u = __float_as_uint(x);

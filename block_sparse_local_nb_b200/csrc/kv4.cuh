@@ -45,6 +45,18 @@ struct Page {
   }
 };
 
+// Extremes that are no number when an operand is none.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Where the tokens of a sequence lie: pages of the pool through a block table.
 struct Pool {
   uint8_t* base;         // [num_pages][kv_heads][page bytes]

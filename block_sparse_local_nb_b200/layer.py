@@ -120,6 +120,12 @@ def block_sparse_local_attention(q, k, v, lengths=None, R: int = 1, causal: bool
     return BlockSparseLocalAttention.apply(q, k, v, lengths, R, causal)
 
 
+def _c_int(x) -> int:
+    """A Python integer as the library's 32-bit one: the nearest (a window or sinks
+    beyond it mean the same, or are refused all the same)."""
+    return max(-2**31, min(int(x), 2**31 - 1))
+
+
 class SinkAttention(torch.autograd.Function):
     """O = softmax(Q K^T / sqrt(d)) V where query q sees key k when k <= q,
     k < lengths[b] and (q - k < window or k < sinks), with its backward.  q is
@@ -137,8 +143,11 @@ class SinkAttention(torch.autograd.Function):
             raise TypeError("q, k, v must share one dtype")
         if not (q.device == k.device == v.device):
             raise ValueError("q, k, v must be on one device")
+        window, sinks = _c_int(window), _c_int(sinks)
         q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
         if lengths is not None:
+            if lengths.shape != (batch,):
+                raise ValueError("lengths must be [batch]")
             lengths = lengths.to(device=q.device, dtype=torch.int32).contiguous()
         o = torch.empty_like(q)
         lse = torch.empty((batch, heads, n), dtype=torch.float32, device=q.device)
@@ -150,6 +159,7 @@ class SinkAttention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse, lengths = ctx.saved_tensors
         batch, heads, n, d = q.shape
@@ -186,11 +196,11 @@ class KV4Cache:
         if batch < 1 or kv_heads < 1 or max_tokens < 1:
             raise ValueError("batch, kv_heads and max_tokens must be positive")
         self.batch, self.kv_heads, self.d = batch, kv_heads, d
-        self.device = torch.device(device)
         self.max_pages = -(-max_tokens // BLOCK)
         self.num_pages = batch * self.max_pages
         self.pool = torch.zeros((self.num_pages, kv_heads, page_bytes), dtype=torch.uint8,
-                                device=self.device)
+                                device=device)
+        self.device = self.pool.device  # with its index, whatever the current device is later
         self.block_table = torch.arange(self.num_pages, dtype=torch.int32,
                                         device=self.device).reshape(batch, self.max_pages)
         self.lengths = torch.zeros(batch, dtype=torch.int32, device=self.device)
@@ -198,7 +208,14 @@ class KV4Cache:
     def _rows(self, x, name):
         if x.dim() != 4 or x.shape[0] != self.batch or x.shape[1] != self.kv_heads or x.shape[3] != self.d:
             raise ValueError(f"{name} must be [{self.batch}, {self.kv_heads}, n, {self.d}]")
+        if x.device != self.device:
+            raise ValueError(f"{name} must be on the cache's device, {self.device}")
         return x.contiguous()
+
+    def _per_sequence(self, x, name):
+        if x.shape != (self.batch,):
+            raise ValueError(f"{name} must be [{self.batch}]")
+        return x.to(device=self.device, dtype=torch.int32).contiguous()
 
     def append(self, k, v, counts=None):
         """Quantise the first ``counts[b]`` (default: all n) tokens of k, v
@@ -209,7 +226,7 @@ class KV4Cache:
             raise ValueError("k and v must share shape and dtype")
         n = k.shape[2]
         if counts is not None:
-            counts = counts.to(device=self.device, dtype=torch.int32).clamp(0, n).contiguous()
+            counts = self._per_sequence(counts, "counts").clamp(0, n)
         with torch.cuda.device(self.device):
             nb.nb_kv4_write(k, v, self.pool, self.block_table, self.lengths, counts, self.batch,
                             self.kv_heads, n, self.d, self.max_pages, self.num_pages,
@@ -222,10 +239,10 @@ class KV4Cache:
         that the cache has from there) are 0."""
         if starts is None:
             starts = torch.zeros_like(self.lengths)
-        starts = starts.to(device=self.device, dtype=torch.int32).contiguous()
+        starts = self._per_sequence(starts, "starts")
         if counts is None:
-            counts = (self.lengths - starts).clamp(0, n)
-        counts = counts.to(device=self.device, dtype=torch.int32).contiguous()
+            counts = (self.lengths.clamp(max=self.max_pages * BLOCK) - starts).clamp(0, n)
+        counts = self._per_sequence(counts, "counts")
         k = torch.empty((self.batch, self.kv_heads, n, self.d), dtype=dtype, device=self.device)
         v = torch.empty_like(k)
         with torch.cuda.device(self.device):
@@ -239,6 +256,9 @@ class KV4Cache:
         window of tokens and its first ``sinks``; [batch, heads, d]."""
         if q.dim() != 3 or q.shape[0] != self.batch or q.shape[2] != self.d:
             raise ValueError(f"q must be [{self.batch}, heads, {self.d}]")
+        if q.device != self.device:
+            raise ValueError(f"q must be on the cache's device, {self.device}")
+        window, sinks = _c_int(window), _c_int(sinks)
         q = q.contiguous()
         heads, code = q.shape[1], _dtype_code(q)
         o = torch.empty_like(q)

@@ -224,6 +224,92 @@ def test_decode_long_in_shares(d, batch, kv_heads, heads, n, window, sinks):
     assert np.array_equal(a, check_decode(c, q, kq, vq, lengths, window, sinks))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("up,down", [(-130, 0), (-100, 0), (60, -60), (118, -118), (0, 40)])
+def test_decode_of_queries_and_keys_of_any_size(up, down, d):
+    """Queries by 2^up (subnormal ones too), keys by 2^down where the product stays
+    moderate; (0, 40): the channels of a query 2^40 apart, one head's query 0.
+    Subnormal fp32 sums keep 2^-18 of a score, well inside the 1e-4."""
+    n, lengths = 192, [192, 70]
+    wide = down > 0
+    c = Cache(2, 2, d, n // PAGE)
+    k = (rows((2, 2, n, d), 5, torch.float32) * 2.0 ** (0 if wide else down)).bfloat16()
+    v = rows((2, 2, n, d), 6, torch.bfloat16)
+    c.write(k.cuda(), v.cuda(), None, i32(lengths))
+    q = torch.randn(2, 6, d, generator=torch.Generator().manual_seed(d)).double()
+    if wide:
+        q[..., ::2] *= 2.0 ** -down
+        q[:, 1] = 0
+    q = (q * 2.0 ** up).bfloat16()
+    check_decode(c, q, kv4.values(k.double().numpy()), kv4.values(v.double().numpy()), lengths, 100, 3)
+
+
+@pytest.mark.parametrize("n", [1, 100, 3000, 20000])  # one warp, a block, a cluster, the workspace
+def test_decode_of_what_is_not_a_number(n):
+    """A key that is no number, where it is visible, makes its head's outputs none; a
+    value makes its group of channels none; where they are hidden nothing changes."""
+    pages = -(-n // PAGE)
+    c = Cache(1, 3, 64, pages)
+    k, v = (rows((1, 3, n, 64), s, torch.bfloat16) for s in (1, 2))
+    k[0, 1, n // 2, 5] = float("inf")
+    v[0, 2, n // 2, 40] = float("nan")
+    c.write(k.cuda(), v.cuda())
+    q = torch.randn(1, 6, 64, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    o, lse = c.decode(q, i32([n]), n, 0)
+    lse, o = lse.isnan()[0].tolist(), o.isnan()[0]
+    assert lse == [False] * 2 + [True] * 2 + [False] * 2
+    assert not o[:2].any() and o[2:4].all() and not o[4:, :32].any() and o[4:, 32:].all()
+    if n > 1:
+        o, lse = c.decode(q, i32([n]), n - 1 - n // 2, 0)
+        assert not o.isnan().any() and not lse.isnan().any()
+
+
+def test_decode_in_graphs_on_streams_and_at_once():
+    """Shares through the workspace: captured and replayed on new inputs, and two calls
+    at once on two streams with a workspace each, give the bits of plain calls."""
+    n, heads = 20000, 4
+    pages = -(-n // PAGE)
+    shape = (1, heads, 1, 64, pages, pages + 3, 1 << 30, 0, nb.NB_BF16)
+    caches, qs, lens, outs, spaces = [], [], [], [], []
+    size = nb.attn_kv4_decode_workspace_size(1, heads, 1, 64, pages, 1 << 30, 0, nb.NB_BF16)
+    assert size > 0
+    for s in range(2):
+        c = Cache(1, 1, 64, pages, seed=s)
+        c.write(rows((1, 1, n, 64), s, torch.bfloat16).cuda(), rows((1, 1, n, 64), 5 + s, torch.bfloat16).cuda())
+        caches.append(c)
+        qs.append(torch.randn(1, heads, 64, generator=torch.Generator().manual_seed(s)).bfloat16().cuda())
+        lens.append(i32([n - 1000 * s]))
+        outs.append((torch.empty_like(qs[s]), torch.empty(1, heads, device="cuda")))
+        spaces.append(torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda"))
+
+    def step(s):
+        nb.nb_attn_kv4_decode(qs[s], caches[s].pool, caches[s].table, lens[s], *outs[s], spaces[s],
+                              size, *shape)
+
+    want = [caches[s].decode(qs[s], lens[s], 1 << 30, 0) for s in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s in range(2):
+            with torch.cuda.stream(streams[s]):
+                step(s)
+    torch.cuda.synchronize()
+    for s in range(2):
+        assert all(torch.equal(x, y) for x, y in zip(outs[s], want[s]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(0)
+    for q, length in ((qs[0], n), (qs[1], 777), (qs[0], 0)):
+        q, now = q.clone(), i32([length])
+        want = caches[0].decode(q, now, 1 << 30, 0)
+        qs[0].copy_(q)
+        lens[0].copy_(now)
+        spaces[0].fill_(0xFF)
+        graph.replay()
+        graph.replay()
+        assert all(torch.equal(x, y) for x, y in zip(outs[0], want))
+
+
 def test_decode_lengths_null_and_clamped():
     c = Cache(2, 1, 64, 2)
     k, v = (rows((2, 1, 64, 64), s, torch.bfloat16) for s in (1, 2))

@@ -177,6 +177,51 @@ def test_sink_oracle_gradients_against_differences():
             assert abs((up - down) / (2 * h) - g[i]) <= 1e-7, i
 
 
+def test_layer_refuses_what_it_cannot_see_through():
+    """Shapes and devices that would send the kernels past a buffer."""
+    from block_sparse_local_nb_b200 import layer
+
+    q, k = torch.zeros(2, 4, 8, 64, dtype=torch.bfloat16), torch.zeros(2, 2, 8, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="lengths"):
+        layer.sink_attention(q, k, k, torch.zeros(1, dtype=torch.int32), 4)
+    with pytest.raises(ValueError):  # not on a GPU
+        layer.sink_attention(q, k, k, torch.zeros(2, dtype=torch.int32), 4)
+    with pytest.raises(ValueError):
+        layer.sink_attention(q, k[:1], k[:1], None, 4)
+    with pytest.raises(TypeError):
+        layer.sink_attention(q, k.float(), k.float(), None, 4)
+    c = layer.KV4Cache(2, 2, 64, 100, device="cpu")
+    with pytest.raises(ValueError, match="device"):
+        c.append(k.to("meta"), k.to("meta"))
+    with pytest.raises(ValueError, match="k must be"):
+        c.append(k[:, :1], k)
+    with pytest.raises(ValueError, match="share"):
+        c.append(k, k[:, :, :4])
+    with pytest.raises(ValueError, match="counts"):
+        c.append(k, k, torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="starts"):
+        c.read(4, starts=torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(ValueError, match="counts"):
+        c.read(4, counts=torch.zeros(2, 1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="q must be"):
+        c.attend(torch.zeros(1, 4, 64, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="device"):
+        c.attend(torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="meta"))
+    for call in (lambda: c.append(k, k), lambda: c.read(4), lambda: c.attend(q[:, :, 0])):
+        with pytest.raises(ValueError):  # a cache that is not on a GPU
+            call()
+    for args in ((0, 1, 64, 1), (1, 0, 64, 1), (1, 1, 96, 1), (1, 1, 64, 0)):
+        with pytest.raises(ValueError):
+            layer.KV4Cache(*args, device="cpu")
+
+
+def test_layer_windows_past_32_bits_are_the_largest():
+    from block_sparse_local_nb_b200 import layer
+
+    assert layer._c_int(10**12) == 2**31 - 1 and layer._c_int(7) == 7
+    assert layer._c_int(-10**12) == -2**31
+
+
 def test_kv4_oracle_cells():
     """Every value is one of 16 equally spaced ones, at most half a step from x, and
     the extremes of the group fit."""
