@@ -511,7 +511,7 @@ __device__ int epi_warps(const Params& p, const Sched& sch, uint32_t base, uint8
     const float f0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - M);
     const float f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - M);
     const float L = l0 * f0 + l1 * f1;
-    const bool has = L > 0.f;  // padding rows and rows without a visible key: 0
+    const bool has = L != 0.f;  // padding rows: 0; a sum that is no number goes on
     const float inv = has ? 1.f / L : 0.f;
     const float g0 = f0 * inv, g1 = f1 * inv;
     if (!all_ok(mbar_wait(bar + 8 * C::bOFull, tc & 1))) return kErrOFull;

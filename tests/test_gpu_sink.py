@@ -209,6 +209,23 @@ def test_other_stream_and_graph_replay():
             assert all(torch.equal(x, y) for x, y in zip(want, first))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,window", [(1, 1), (300, 50), (1000, 400)])
+def test_what_is_not_a_number_reaches_the_rows_that_see_it(n, window, d):
+    q, k, v, _ = (x.cuda() for x in inputs(1, 2, 2, n, d, 0))
+    want, _ = run_fwd(q, k, v, None, window, 0)
+    at = n // 2
+    q[0, 0, at, 3] = float("nan")
+    k[0, 1, at, 5] = float("nan")
+    o, lse = run_fwd(q, k, v, None, window, 0)
+    seen = torch.zeros(2, n, dtype=torch.bool, device="cuda")
+    seen[0, at] = True
+    seen[1, at:at + window] = True
+    assert torch.equal(o[0].isnan(), seen[..., None].expand(-1, -1, d))
+    assert torch.equal(lse[0].isnan(), seen)
+    assert torch.equal(o[0][~seen], want[0][~seen])
+
+
 def test_autograd_on_strided_inputs():
     """The layer's function on [batch, n, heads, d] storage, against the direct calls."""
     from block_sparse_local_nb_b200.layer import sink_attention
