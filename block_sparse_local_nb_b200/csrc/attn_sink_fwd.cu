@@ -4,11 +4,12 @@
 // k < sinks); S = Q K^T / sqrt(d), online softmax, O = P V, lse.
 //
 // Work item = one query tile of 128 rows of one (sequence, query head).  Its keys
-// are the tokens [q0 - window + 1, q0 + 127] clipped to the sequence, in chunks of
-// 128 from exactly that first token (a TMA box may start at any row), and, when
-// they begin past token 128, one chunk more that holds the sinks.  Every chunk
-// between the window's edge and the diagonal is visible to all rows and takes no
-// mask; in the others a row's visible columns are one 64-bit word per half.
+// are the tokens [q0 - window + 1, q0 + 127] clipped to the sequence, in blocks of
+// 64 from exactly that first token (a TMA box may start at any row), and before
+// them, when they begin past the sinks' blocks, one or two blocks of sinks.  A
+// chunk is two blocks, wherever they lie.  A block between the window's edge and
+// the diagonal is visible to all rows and takes no mask; in the others a row's
+// visible columns are one 64-bit word.
 // A persistent grid of one CTA per SM walks the items, the longest (last) tiles
 // of a sequence first and every second round of items in reverse, so that the
 // SMs' totals differ by little; the heads that share a key/value head follow one
@@ -49,7 +50,8 @@ using namespace sm100;
 constexpr int kThreads = 512;
 constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;  // per thread at launch
 constexpr int kRows = 128;   // query rows per tile
-constexpr int kChunk = 128;  // keys per chunk
+constexpr int kHalf = 64;    // keys of a block
+constexpr int kChunk = 128;  // keys of a chunk: two blocks
 constexpr int kSlab = 128 * 128;  // one swizzled box: 128 rows x 64 bf16
 constexpr float kTau = 8.0f;      // lazy-rescale threshold, log2 units
 constexpr float kLog2e = 1.4426950408889634f;
@@ -110,10 +112,13 @@ struct Params {
 
 struct Item {
   int b, h, tile, L;
-  int k0;    // first key of the window's chunks
-  int far;   // 1: a chunk of the sinks (keys 0..127) comes before them
-  int nch;   // chunks, 0 for a tile past the sequence's length
-  __device__ __forceinline__ int key(int c) const { return c < far ? 0 : k0 + (c - far) * kChunk; }
+  int k0;    // first key of the window's blocks
+  int far;   // blocks of sinks (keys 0.. and 64..) before them
+  int nch;   // chunks of two blocks, 0 for a tile past the sequence's length
+  // first of the 64 keys of block i; the last chunk's second may lie past the tile's keys
+  __device__ __forceinline__ int key(int i) const {
+    return i < far ? i * kHalf : k0 + (i - far) * kHalf;
+  }
 };
 
 __device__ __forceinline__ Item decode_bht(const Params& p, int b, int h, int tile, int L) {
@@ -128,11 +133,12 @@ __device__ __forceinline__ Item decode_bht(const Params& p, int b, int h, int ti
     // tokens below k0 are outside every row's window
     x.k0 = q0 >= p.window ? q0 - p.window + 1 : 0;
     if (p.sinks > 0 && x.k0 > 0) {
-      if (x.k0 <= kChunk) x.k0 = 0;  // one chunk more either way: no separate one
-      else x.far = 1;
+      const int f = (p.sinks + kHalf - 1) / kHalf;
+      if (x.k0 <= f * kHalf) x.k0 = 0;  // no more blocks than with separate ones
+      else x.far = f;
     }
     const int end = min(q0 + kRows, L);
-    x.nch = x.far + (end - x.k0 + kChunk - 1) / kChunk;
+    x.nch = (x.far + (end - x.k0 + kHalf - 1) / kHalf + 1) / 2;
   }
   return x;
 }
@@ -192,8 +198,11 @@ __device__ int producer(const Params& p, const Sched& sch, uint32_t base, const 
       const uint32_t full = bar + 8 * (C::bKFull + st);
       mbar_arrive_expect_tx(full, C::kKBytes);
 #pragma unroll
-      for (int s = 0; s < D / 64; ++s)
-        tma_load_3d(base + C::oK + st * C::kKBytes + s * kSlab, tk, full, s * 64, x.key(c), bkv);
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int s = 0; s < D / 64; ++s)
+          tma_load_3d(base + C::oK + st * C::kKBytes + s * kSlab + h * kHalf * 128, tk, full, s * 64,
+                      x.key(2 * c + h), bkv);
     }
     g += x.nch;
     ++tc;
@@ -215,8 +224,10 @@ __device__ int v_producer(const Params& p, const Sched& sch, uint32_t base, uint
     if (x.nch == 0) continue;
     const int bkv = (x.b * p.a.heads + x.h) / p.group;
     for (int c = 0; c < x.nch; ++c) {
-      const int G = g + c, st = G % C::NKV, y = x.key(c);
-      const bool fix = y + kChunk > x.L && x.L < p.a.n;  // rows [L - y, 128) hold other data
+      const int G = g + c, st = G % C::NKV;
+      const int y[2] = {x.key(2 * c), x.key(2 * c + 1)};
+      // rows of a block from L - y on hold other data
+      const bool fix = max(y[0], y[1]) + kHalf > x.L && x.L < p.a.n;
       const uint32_t full = bar + 8 * (C::bVFull + st);
       const uint32_t land = fix ? bar + 8 * C::bVFix : full;
       bool ok = true;
@@ -225,8 +236,11 @@ __device__ int v_producer(const Params& p, const Sched& sch, uint32_t base, uint
         if (ok) {
           mbar_arrive_expect_tx(land, C::kKBytes);
 #pragma unroll
-          for (int s = 0; s < D / 64; ++s)
-            tma_load_3d(base + C::oV + st * C::kKBytes + s * kSlab, tv, land, s * 64, y, bkv);
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int s = 0; s < D / 64; ++s)
+              tma_load_3d(base + C::oV + st * C::kKBytes + s * kSlab + h * kHalf * 128, tv, land,
+                          s * 64, y[h], bkv);
         }
       }
       if (!__all_sync(0xffffffffu, ok)) return kErrVFree;
@@ -234,10 +248,10 @@ __device__ int v_producer(const Params& p, const Sched& sch, uint32_t base, uint
         if (!__all_sync(0xffffffffu, mbar_wait(land, fixes & 1))) return kErrVFix;
         ++fixes;
         uint4* v = reinterpret_cast<uint4*>(gbase + C::oV + st * C::kKBytes);
-        const int r0 = x.L - y;  // whole 128-byte rows, so the swizzle does not matter
-        for (int s = 0; s < D / 64; ++s)
-          for (int i = r0 * 8 + lane; i < kChunk * 8; i += 32)
-            v[s * (kSlab / 16) + i] = make_uint4(0, 0, 0, 0);
+        for (int h = 0; h < 2; ++h)  // whole 128-byte rows, so the swizzle does not matter
+          for (int s = 0; s < D / 64; ++s)
+            for (int i = max(x.L - y[h], 0) * 8 + lane; i < kHalf * 8; i += 32)
+              v[s * (kSlab / 16) + h * kHalf * 8 + i] = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(full);
@@ -352,7 +366,7 @@ __device__ int softmax_warps(const Params& p, const Sched& sch, uint32_t base, u
   int g = 0, tc = 0;
   for (int rd = 0, it; (it = item_at(rd)) < sch.count; ++rd) {
     const Item x = sched_item(p, sch, it);
-    const int q0 = x.tile * kRows, q = q0 + r;
+    const int q0 = x.tile * kRows, q = q0 + r, qw = q0 + wq * 32;  // qw: the warp's first row
     if (x.nch == 0) {  // the whole tile is padding
       zero_tile(x);
       continue;
@@ -361,15 +375,19 @@ __device__ int softmax_warps(const Params& p, const Sched& sch, uint32_t base, u
     float m_used = -INFINITY, l = 0.f;
     for (int c = 0; c < x.nch; ++c) {
       const int G = g + c, sb = G % C::NSB;
-      const int kc = x.key(c) + 64 * hf;  // this half's first key
-      // keys visible to every row of the tile: none after the first row, none at
-      // or before the last row's window edge, all below the length
-      const bool whole = c >= x.far && kc + 63 <= q0 && kc > q0 + kRows - 1 - p.window &&
-                         q0 + kRows <= x.L;
+      const int blk = 2 * c + hf, kc = x.key(blk);  // this half's block and its first key
+      // 32 keys visible to every row of the warp: none after its first row, none at or
+      // before its last row's window edge, and all its rows below the length.  (The
+      // bits of a mask cost two instructions a key, a quarter of the warp's time.)
+      bool whole[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        whole[j] = blk >= x.far && kc + 32 * j + 31 <= qw && kc + 32 * j > qw + 31 - p.window &&
+                   qw + 32 <= x.L;
       uint64_t mask = ~0ull;
-      if (!whole) {
+      if (!(whole[0] && whole[1])) {
         const int first = q >= p.window ? q - p.window + 1 : 0;
-        if (c < x.far) mask = bit_range(-kc, p.sinks - kc);
+        if (blk < x.far) mask = bit_range(-kc, p.sinks - kc);
         else mask = bit_range(first - kc, q + 1 - kc) |
                     (x.far ? 0ull : bit_range(-kc, min(p.sinks, q + 1) - kc));
         if (q >= x.L) mask = 0ull;
@@ -390,9 +408,9 @@ __device__ int softmax_warps(const Params& p, const Sched& sch, uint32_t base, u
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const uint32_t mw = static_cast<uint32_t>(mask >> (32 * j));
-        vis[j] = whole || __any_sync(0xffffffffu, mw != 0u);
+        vis[j] = whole[j] || __any_sync(0xffffffffu, mw != 0u);
         if (vis[j]) {
-          if (!whole) {
+          if (!whole[j]) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) s[j][i] = (mw >> i) & 1u ? s[j][i] : -INFINITY;
           }
@@ -650,8 +668,8 @@ cudaError_t launch(const SinkArgs& g, cudaStream_t stream) {
   const int64_t kv_total = static_cast<int64_t>(g.batch) * g.kv_heads;
   CUtensorMap tq, tk, tv, to;
   if (!make_tmap_bf16_rows(&tq, g.q, D, g.n, heads_total, kRows) ||
-      !make_tmap_bf16_rows(&tk, g.k, D, g.n, kv_total, kChunk) ||
-      !make_tmap_bf16_rows(&tv, g.v, D, g.n, kv_total, kChunk) ||
+      !make_tmap_bf16_rows(&tk, g.k, D, g.n, kv_total, kHalf) ||
+      !make_tmap_bf16_rows(&tv, g.v, D, g.n, kv_total, kHalf) ||
       !make_tmap_bf16_rows(&to, g.o, D, g.n, heads_total, kRows))
     return cudaErrorInvalidValue;
   Params p;
