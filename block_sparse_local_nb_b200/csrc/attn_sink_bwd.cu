@@ -309,20 +309,6 @@ __device__ __forceinline__ Chunk chunk(const Params& p, const Item& x, int c) {
 enum : int { kErrTFree = 0x81, kErrXFree, kErrFix, kErrTFull, kErrXFull, kErrSFree, kErrPFull, kErrAFree,
              kErrSFull, kErrYFree, kErrYFull, kErrDone, kErrIFree, kErrIFull, kErrGTFull, kErrAFull };
 
-// Position in a ring of N barriers and the parity of its current pass.
-template <int N>
-struct Ring {
-  int i = 0;
-  uint32_t ph = 0;
-  __device__ __forceinline__ void next(int step = 1) {  // step <= N
-    i += step;
-    if (i >= N) {
-      i -= N;
-      ph ^= 1;
-    }
-  }
-};
-
 // A chunk's operands into their stages (whole warp; lane 0 issues): one, or where
 // map1 is not null two.  Where the chunk reaches past the length (other data lies
 // there: P is 0, but 0 x NaN is not) they land on `fixbar`, and the warp zeroes the

@@ -53,6 +53,8 @@ constexpr int kRows = 128;   // query rows per tile
 constexpr int kHalf = 64;    // keys of a block
 constexpr int kChunk = 128;  // keys of a chunk: two blocks
 constexpr int kSlab = 128 * 128;  // one swizzled box: 128 rows x 64 bf16
+constexpr int kItems = 4;          // items decoded ahead
+constexpr int kTakers = 15;         // arrivals that free one: V producer, 2 issuers, 8 + 4 warps
 constexpr float kTau = 8.0f;      // lazy-rescale threshold, log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -62,26 +64,29 @@ struct Cfg {
   static constexpr int NQ = D == 64 ? 2 : 1;   // Q tile buffers
   static constexpr int NKV = D == 64 ? 3 : 2;  // K chunk stages, and as many V chunk stages
   static constexpr int NSB = NKV;              // S buffers
-  static constexpr int NOB = 1;  // O accumulators per half (tiles in flight)
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kKBytes = kChunk * D * 2;
   static constexpr int oQ = 0;
   static constexpr int oK = oQ + NQ * kQBytes;
   static constexpr int oV = oK + NKV * kKBytes;
   static constexpr int oStg = oV + NKV * kKBytes;  // output tile staging (D / 64 boxes)
-  static constexpr int oBar = oStg + kRows * D * 2;
+  static constexpr int oItem = oStg + kRows * D * 2;  // ring of items
+  static constexpr int oBar = oItem + kItems * 32;
+  static_assert(oItem % 16 == 0, "items are read 16 bytes at once");
   // barrier indices ([S buffer][half] for P, [half][buffer] for O)
   static constexpr int bQFull = 0, bQFree = bQFull + NQ, bKFull = bQFree + NQ,
                        bVFull = bKFull + NKV, bSFull = bVFull + NKV, bSFree = bSFull + NSB,
                        bPFull = bSFree + NSB, bOFull = bPFull + NSB, bOFree = bOFull + 1,
                        bXFull = bOFree + 1, bXFree = bXFull + 2,
-                       bVFix = bXFree + 2, bDone = bVFix + 1, nBar = bDone + 1;
+                       bIFull = bXFree + 2, bIFree = bIFull + kItems, bVFix = bIFree + kItems,
+                       bDone = bVFix + 1, nBar = bDone + 1;
   static constexpr int oSlot = oBar + nBar * 8;
   // per-tile hand-off of the halves' running max and sum to the epilogue warps:
   // [parity][half][m, l][row] fp32
   static constexpr int oXSum = oSlot + 16;
   static constexpr int oSched = oXSum + 2 * 2 * 2 * 128 * 4;  // work-order prefix table
   static constexpr int kSmem = oSched + kSchedBytes + 1024;  // + slack for 1024-byte alignment
+  static_assert(oXSum % 4 == 0 && oSched % 4 == 0, "words");
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
   static constexpr uint32_t kTmemCols = 512;
   // S buffer i: columns [128 i, 128 i + 128).  Half h's P (64 keys, two bf16
@@ -90,9 +95,8 @@ struct Cfg {
   // 2 x 128).
   static constexpr uint32_t tS = 0;
   __device__ static constexpr uint32_t tP(int sb, int h) { return tS + sb * kChunk + 64 * h; }
-  // O accumulator of half h, buffer ob
-  __device__ static constexpr uint32_t tO(int h, int ob) { return NSB * kChunk + (h * NOB + ob) * D; }
-  static_assert(NSB * kChunk + 2 * NOB * D <= kTmemCols, "tensor memory columns");
+  __device__ static constexpr uint32_t tO(int h) { return NSB * kChunk + h * D; }
+  static_assert(NSB * kChunk + 2 * D <= kTmemCols, "tensor memory columns");
   // registers per thread after reallocation: TMA/MMA warpgroup, each softmax
   // warpgroup, epilogue warpgroup (the 16 warps share the 64K-register file;
   // the d = 128 softmax spills less with 176, the d = 64 one runs faster at 168)
@@ -110,7 +114,7 @@ struct Params {
   int items;   // batch * heads * ntiles
 };
 
-struct Item {
+struct alignas(16) Item {
   int b, h, tile, L;
   int k0;    // first key of the window's blocks
   int far;   // blocks of sinks (keys 0.. and 64..) before them
@@ -173,39 +177,78 @@ __device__ __forceinline__ Item sched_item(const Params& p, const Sched& s, int 
 // error codes: 0x60 + site
 enum : int { kErrQFree = 0x61, kErrKFree, kErrQFull, kErrKFull, kErrSFree, kErrOFree, kErrPFull,
              kErrSFull, kErrPPrev, kErrOFull, kErrDone, kErrXFull, kErrXFree, kErrVFree, kErrVFull,
-             kErrVFix };
+             kErrVFix, kErrIFree, kErrIFull };
 
+static_assert(sizeof(Item) <= 32, "slot of the ring");
+
+// The rd-th item of this CTA from the ring, for the warps that work on it; x.nch < 0
+// after the last.  Called by whole warps.
 template <int D>
-__device__ int producer(const Params& p, const Sched& sch, uint32_t base, const CUtensorMap* tq,
-                        const CUtensorMap* tk) {
+__device__ __forceinline__ bool next_item(Item& x, int rd, uint32_t bar, const uint8_t* gbase,
+                                          int lane) {
+  using C = Cfg<D>;
+  const int i = rd % kItems;
+  if (!__all_sync(0xffffffffu, mbar_wait(bar + 8 * (C::bIFull + i), (rd / kItems) & 1)))
+    return false;
+  x = *reinterpret_cast<const Item*>(gbase + C::oItem + i * 32);
+  __syncwarp();  // every lane has read it
+  if (lane == 0) mbar_arrive(bar + 8 * (C::bIFree + i));
+  return true;
+}
+
+// Number of chunks of the rd-th item, for the single-thread roles; < 0 after the last,
+// kNoItem on a timeout.
+constexpr int kNoItem = -2;
+template <int D>
+__device__ __forceinline__ int next_chunks(int rd, uint32_t bar, const uint8_t* gbase) {
+  using C = Cfg<D>;
+  const int i = rd % kItems;
+  if (!mbar_wait(bar + 8 * (C::bIFull + i), (rd / kItems) & 1)) return kNoItem;
+  const int nch = reinterpret_cast<const Item*>(gbase + C::oItem + i * 32)->nch;
+  mbar_arrive(bar + 8 * (C::bIFree + i));
+  return nch;
+}
+
+// Items, Q tiles and K chunks (warp 0, one thread).  An item is decoded once, here,
+// and handed to the other roles through a ring: its search and divisions take a
+// thousand cycles, which each role spent between two tiles before.
+template <int D>
+__device__ int producer(const Params& p, const Sched& sch, uint32_t base, uint8_t* gbase,
+                        const CUtensorMap* tq, const CUtensorMap* tk) {
   using C = Cfg<D>;
   const uint32_t bar = base + C::oBar;
-  int g = 0, tc = 0;
-  for (int rd = 0, it; (it = item_at(rd)) < sch.count; ++rd) {
-    const Item x = sched_item(p, sch, it);
+  Ring<C::NQ> qr;
+  Ring<C::NKV> kr;
+  for (int rd = 0;; ++rd) {
+    const int it = item_at(rd), i = rd % kItems;
+    Item x;
+    if (it < sch.count) x = sched_item(p, sch, it);
+    else x.nch = -1;
+    if (!mbar_wait(bar + 8 * (C::bIFree + i), ((rd / kItems) & 1) ^ 1)) return kErrIFree;
+    *reinterpret_cast<Item*>(gbase + C::oItem + i * 32) = x;
+    mbar_arrive(bar + 8 * (C::bIFull + i));
+    if (x.nch < 0) break;
     if (x.nch == 0) continue;
     const int bh = x.b * p.a.heads + x.h, bkv = bh / p.group;
-    const int qs = tc % C::NQ;
-    if (!mbar_wait(bar + 8 * (C::bQFree + qs), ((tc / C::NQ) & 1) ^ 1)) return kErrQFree;
-    mbar_arrive_expect_tx(bar + 8 * (C::bQFull + qs), C::kQBytes);
+    if (!mbar_wait(bar + 8 * (C::bQFree + qr.i), qr.ph ^ 1)) return kErrQFree;
+    mbar_arrive_expect_tx(bar + 8 * (C::bQFull + qr.i), C::kQBytes);
 #pragma unroll
     for (int s = 0; s < D / 64; ++s)
-      tma_load_3d(base + C::oQ + qs * C::kQBytes + s * kSlab, tq, bar + 8 * (C::bQFull + qs),
+      tma_load_3d(base + C::oQ + qr.i * C::kQBytes + s * kSlab, tq, bar + 8 * (C::bQFull + qr.i),
                   s * 64, x.tile * kRows, bh);
+    qr.next();
     for (int c = 0; c < x.nch; ++c) {
-      const int G = g + c, st = G % C::NKV;
-      if (!mbar_wait(bar + 8 * (C::bSFull + st), ((G / C::NKV) & 1) ^ 1)) return kErrKFree;
-      const uint32_t full = bar + 8 * (C::bKFull + st);
+      if (!mbar_wait(bar + 8 * (C::bSFull + kr.i), kr.ph ^ 1)) return kErrKFree;
+      const uint32_t full = bar + 8 * (C::bKFull + kr.i);
       mbar_arrive_expect_tx(full, C::kKBytes);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int s = 0; s < D / 64; ++s)
-          tma_load_3d(base + C::oK + st * C::kKBytes + s * kSlab + h * kHalf * 128, tk, full, s * 64,
-                      x.key(2 * c + h), bkv);
+          tma_load_3d(base + C::oK + kr.i * C::kKBytes + s * kSlab + h * kHalf * 128, tk, full,
+                      s * 64, x.key(2 * c + h), bkv);
+      kr.next();
     }
-    g += x.nch;
-    ++tc;
   }
   return 0;
 }
@@ -214,17 +257,19 @@ __device__ int producer(const Params& p, const Sched& sch, uint32_t base, const 
 // the sequence's length lands on a barrier of its own; the warp zeroes the rows
 // past the length and then hands the chunk on.
 template <int D>
-__device__ int v_producer(const Params& p, const Sched& sch, uint32_t base, uint8_t* gbase,
-                          int lane, const CUtensorMap* tv) {
+__device__ int v_producer(const Params& p, uint32_t base, uint8_t* gbase, int lane,
+                          const CUtensorMap* tv) {
   using C = Cfg<D>;
   const uint32_t bar = base + C::oBar;
-  int g = 0, fixes = 0;
-  for (int rd = 0, it; (it = item_at(rd)) < sch.count; ++rd) {
-    const Item x = sched_item(p, sch, it);
-    if (x.nch == 0) continue;
+  int fixes = 0;
+  Ring<C::NKV> vr;
+  for (int rd = 0;; ++rd) {
+    Item x;
+    if (!next_item<D>(x, rd, bar, gbase, lane)) return kErrIFull;
+    if (x.nch < 0) break;
     const int bkv = (x.b * p.a.heads + x.h) / p.group;
     for (int c = 0; c < x.nch; ++c) {
-      const int G = g + c, st = G % C::NKV;
+      const int st = vr.i;
       const int y[2] = {x.key(2 * c), x.key(2 * c + 1)};
       // rows of a block from L - y on hold other data
       const bool fix = max(y[0], y[1]) + kHalf > x.L && x.L < p.a.n;
@@ -232,7 +277,7 @@ __device__ int v_producer(const Params& p, const Sched& sch, uint32_t base, uint
       const uint32_t land = fix ? bar + 8 * C::bVFix : full;
       bool ok = true;
       if (lane == 0) {
-        ok = mbar_wait(bar + 8 * (C::bSFree + st), ((G / C::NKV) & 1) ^ 1);
+        ok = mbar_wait(bar + 8 * (C::bSFree + st), vr.ph ^ 1);
         if (ok) {
           mbar_arrive_expect_tx(land, C::kKBytes);
 #pragma unroll
@@ -256,8 +301,8 @@ __device__ int v_producer(const Params& p, const Sched& sch, uint32_t base, uint
         __syncwarp();
         if (lane == 0) mbar_arrive(full);
       }
+      vr.next();
     }
-    g += x.nch;
   }
   return 0;
 }
@@ -265,72 +310,83 @@ __device__ int v_producer(const Params& p, const Sched& sch, uint32_t base, uint
 // S = Q K^T for every chunk into S buffer G % NSB (warp 1, one thread).  P of
 // chunk G replaces S in that buffer, so S of chunk G + NSB waits for P V of
 // chunk G, which the other issuer signals on bSFree.
+// A lone thread takes four cycles and more an instruction, on the chain from P to the
+// next S: positions advance by steps, descriptors by adds.
 template <int D>
-__device__ int s_issuer(const Params& p, const Sched& sch, uint32_t base, uint32_t tmem) {
+__device__ int s_issuer(uint32_t base, const uint8_t* gbase, uint32_t tmem) {
   using C = Cfg<D>;
   const uint32_t bar = base + C::oBar;
   constexpr uint32_t kIdS = idesc_bf16_f32(128, kChunk, false, false);  // Q K^T: both K-major
-  int g = 0, tc = 0;
-  for (int rd = 0, it; (it = item_at(rd)) < sch.count; ++rd) {
-    const Item x = sched_item(p, sch, it);
-    if (x.nch == 0) continue;
-    const int qs = tc % C::NQ;
-    if (!mbar_wait(bar + 8 * (C::bQFull + qs), (tc / C::NQ) & 1)) return kErrQFull;
-    const uint64_t dQ = smem_desc_sw128(base + C::oQ + qs * C::kQBytes, 0, 1024);
-    for (int c = 0; c < x.nch; ++c) {
-      const int G = g + c, st = G % C::NKV, sb = G % C::NSB;
-      const uint64_t dK = smem_desc_sw128(base + C::oK + st * C::kKBytes, 0, 1024);
-      const uint32_t tD = tmem + C::tS + sb * kChunk;
-      if (!mbar_wait(bar + 8 * (C::bKFull + st), (G / C::NKV) & 1)) return kErrKFull;
-      if (!mbar_wait(bar + 8 * (C::bSFree + sb), ((G / C::NSB) & 1) ^ 1)) return kErrSFree;
+  const uint64_t dQ0 = smem_desc_sw128(base + C::oQ, 0, 1024);
+  const uint64_t dK0 = smem_desc_sw128(base + C::oK, 0, 1024);
+  Ring<C::NQ> qr;
+  Ring<C::NKV> kr;  // K stage and S buffer
+  for (int rd = 0;; ++rd) {
+    const int nch = next_chunks<D>(rd, bar, gbase);
+    if (nch == kNoItem) return kErrIFull;
+    if (nch < 0) break;
+    if (nch == 0) continue;
+    if (!mbar_wait(bar + 8 * (C::bQFull + qr.i), qr.ph)) return kErrQFull;
+    const uint64_t dQ = desc_add(dQ0, qr.i * (C::kQBytes >> 4));
+    for (int c = 0; c < nch; ++c) {
+      const uint64_t dK = desc_add(dK0, kr.i * (C::kKBytes >> 4));
+      const uint32_t tD = tmem + C::tS + kr.i * kChunk;
+      const uint32_t kfull = bar + 8 * (C::bKFull + kr.i), sfree = bar + 8 * (C::bSFree + kr.i);
+      // both are asked before the first answer is looked at
+      const bool okk = mbar_try_wait(kfull, kr.ph), oks = mbar_try_wait(sfree, kr.ph ^ 1);
+      if (!okk && !mbar_wait(kfull, kr.ph)) return kErrKFull;
+      if (!oks && !mbar_wait(sfree, kr.ph ^ 1)) return kErrSFree;
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint32_t off = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;  // descriptor address units
         mma_bf16_ss(tD, desc_add(dQ, off), desc_add(dK, off), kIdS, k > 0);
       }
-      mma_commit(bar + 8 * (C::bSFull + sb));  // also frees the K stage: its only reader
-      if (c == x.nch - 1) mma_commit(bar + 8 * (C::bQFree + qs));  // the tile's S products issued
+      mma_commit(bar + 8 * (C::bSFull + kr.i));  // also frees the K stage: its only reader
+      if (c == nch - 1) mma_commit(bar + 8 * (C::bQFree + qr.i));  // the tile's S products issued
+      kr.next();
     }
-    g += x.nch;
-    ++tc;
+    qr.next();
   }
   return 0;
 }
 
-// O_h += P_h V_h for every chunk and half (warp 10, one thread): P from TMEM,
-// V from shared memory.  Completion of chunk G's products frees its S buffer
-// and its K/V stage (S of chunk G completed before its softmax began).
+// O_h += P_h V_h for every chunk and half (warp 2, one thread): P from TMEM,
+// V from shared memory.  Completion of a chunk's products frees its S buffer
+// and its V stage (its S completed before its softmax began).
 template <int D>
-__device__ int pv_issuer(const Params& p, const Sched& sch, uint32_t base, uint32_t tmem) {
+__device__ int pv_issuer(uint32_t base, const uint8_t* gbase, uint32_t tmem) {
   using C = Cfg<D>;
   const uint32_t bar = base + C::oBar;
   constexpr uint32_t kIdPV = idesc_bf16_f32(128, D, false, true);  // V is MN-major (K = 64 per half)
-  int g = 0, tc = 0;
-  for (int rd = 0, it; (it = item_at(rd)) < sch.count; ++rd) {
-    const Item x = sched_item(p, sch, it);
-    if (x.nch == 0) continue;
-    for (int c = 0; c < x.nch; ++c) {
-      const int G = g + c, st = G % C::NKV, sb = G % C::NSB;
-      // V is MN-major: 64-column swizzle atoms kSlab apart, 8-key groups 1024 bytes apart
-      const uint64_t dV = smem_desc_sw128(base + C::oV + st * C::kKBytes, kSlab, 1024);
-      if (!mbar_wait(bar + 8 * (C::bVFull + st), (G / C::NKV) & 1)) return kErrVFull;
-      if (c == 0 && !mbar_wait(bar + 8 * C::bOFree, (tc & 1) ^ 1)) return kErrOFree;
-      if (!mbar_wait(bar + 8 * (C::bPFull + sb), (G / C::NSB) & 1)) return kErrPFull;
+  // V is MN-major: 64-column swizzle atoms kSlab apart, 8-key groups 1024 bytes apart
+  const uint64_t dV0 = smem_desc_sw128(base + C::oV, kSlab, 1024);
+  Ring<C::NKV> vr;  // V stage and S buffer
+  Ring<1> o;
+  for (int rd = 0;; ++rd) {
+    const int nch = next_chunks<D>(rd, bar, gbase);
+    if (nch == kNoItem) return kErrIFull;
+    if (nch < 0) break;
+    if (nch == 0) continue;
+    if (!mbar_wait(bar + 8 * C::bOFree, o.ph ^ 1)) return kErrOFree;
+    for (int c = 0; c < nch; ++c) {
+      const uint64_t dV = desc_add(dV0, vr.i * (C::kKBytes >> 4));
+      const uint32_t tP0 = tmem + C::tS + vr.i * kChunk;
+      if (!mbar_wait(bar + 8 * (C::bVFull + vr.i), vr.ph)) return kErrVFull;
+      if (!mbar_wait(bar + 8 * (C::bPFull + vr.i), vr.ph)) return kErrPFull;
       tc_fence_after();
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {  // each half's 64 keys into its own O accumulator
-        const uint32_t tO = tmem + C::tO(h, 0), tP = tmem + C::tP(sb, h);
+      for (int h = 0; h < 2; ++h)  // each half's 64 keys into its own O accumulator
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // 16 keys = 8 P columns = 2048 bytes of V per step
-          mma_bf16_ts(tO, tP + 8 * k, desc_add(dV, (h * 8192 + k * 2048) >> 4), kIdPV, c > 0 || k > 0);
-      }
+          mma_bf16_ts(tmem + C::tO(h), tP0 + 64 * h + 8 * k, desc_add(dV, (h * 8192 + k * 2048) >> 4),
+                      kIdPV, c > 0 || k > 0);
       // frees the S buffer and the V stage, and tells the softmax warps that O may be rescaled
-      mma_commit(bar + 8 * (C::bSFree + sb));
-      if (c == x.nch - 1) mma_commit(bar + 8 * C::bOFull);
+      mma_commit(bar + 8 * (C::bSFree + vr.i));
+      if (c == nch - 1) mma_commit(bar + 8 * C::bOFull);
+      vr.next();
     }
-    g += x.nch;
-    ++tc;
+    o.next();
   }
   return 0;
 }
@@ -363,18 +419,20 @@ __device__ int softmax_warps(const Params& p, const Sched& sch, uint32_t base, u
     for (int i = hf * 128 + r; i < rows * (D / 8); i += 256) out[i] = make_uint4(0, 0, 0, 0);
     if (a.lse && hf == 0 && r < rows) a.lse[row0 + r] = -INFINITY;
   };
-  int g = 0, tc = 0;
-  for (int rd = 0, it; (it = item_at(rd)) < sch.count; ++rd) {
-    const Item x = sched_item(p, sch, it);
+  Ring<C::NSB> sr;
+  int tc = 0;
+  for (int rd = 0;; ++rd) {
+    Item x;
+    if (!next_item<D>(x, rd, bar, gbase, lane)) return kErrIFull;
+    if (x.nch < 0) break;
     const int q0 = x.tile * kRows, q = q0 + r, qw = q0 + wq * 32;  // qw: the warp's first row
     if (x.nch == 0) {  // the whole tile is padding
       zero_tile(x);
       continue;
     }
-    const int ob = tc % C::NOB;
     float m_used = -INFINITY, l = 0.f;
     for (int c = 0; c < x.nch; ++c) {
-      const int G = g + c, sb = G % C::NSB;
+      const int sb = sr.i;
       const int blk = 2 * c + hf, kc = x.key(blk);  // this half's block and its first key
       // 32 keys visible to every row of the warp: none after its first row, none at or
       // before its last row's window edge, and all its rows below the length.  (The
@@ -392,7 +450,7 @@ __device__ int softmax_warps(const Params& p, const Sched& sch, uint32_t base, u
                     (x.far ? 0ull : bit_range(-kc, min(p.sinks, q + 1) - kc));
         if (q >= x.L) mask = 0ull;
       }
-      if (!all_ok(mbar_wait(bar + 8 * (C::bSFull + sb), (G / C::NSB) & 1))) return kErrSFull;
+      if (!all_ok(mbar_wait(bar + 8 * (C::bSFull + sb), sr.ph))) return kErrSFull;
       tc_fence_after();
       float s[2][32];
 #pragma unroll
@@ -453,12 +511,13 @@ __device__ int softmax_warps(const Params& p, const Sched& sch, uint32_t base, u
       }
       if (__any_sync(0xffffffffu, need)) {
         // this half's previous P V product must have landed before its O is rescaled
-        // (need implies c > 0, so chunk G - 1 belongs to this tile)
-        const int Gp = G - 1;
-        if (!all_ok(mbar_wait(bar + 8 * (C::bSFree + Gp % C::NSB), (Gp / C::NSB) & 1)))
+        // (need implies c > 0, so the chunk before belongs to this tile)
+        const bool wrap = sr.i == 0;
+        if (!all_ok(mbar_wait(bar + 8 * (C::bSFree + (wrap ? C::NSB : sr.i) - 1),
+                              wrap ? sr.ph ^ 1 : sr.ph)))
           return kErrPPrev;
         tc_fence_after();
-        const uint32_t to = trow + C::tO(hf, ob);
+        const uint32_t to = trow + C::tO(hf);
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
           float ov[32];
@@ -478,6 +537,7 @@ __device__ int softmax_warps(const Params& p, const Sched& sch, uint32_t base, u
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(bar + 8 * (C::bPFull + sb));
+      sr.next();
     }
     // hand this half's (m, l) of the row to the epilogue warps
     const int par = tc & 1;
@@ -485,7 +545,6 @@ __device__ int softmax_warps(const Params& p, const Sched& sch, uint32_t base, u
     xs[((par * 2 + hf) * 2 + 0) * 128 + r] = m_used;
     xs[((par * 2 + hf) * 2 + 1) * 128 + r] = l;
     mbar_arrive(bar + 8 * (C::bXFull + par));
-    g += x.nch;
     ++tc;
   }
   if (sch.balanced) {  // second pass: the empty tiles, listed directly
@@ -504,8 +563,8 @@ __device__ int softmax_warps(const Params& p, const Sched& sch, uint32_t base, u
 // memory and write it with one TMA tensor store.  Off the softmax warps' path:
 // they hand over (m, l) and move on to the next tile.
 template <int D>
-__device__ int epi_warps(const Params& p, const Sched& sch, uint32_t base, uint8_t* gbase,
-                         uint32_t tmem, int wq, int lane, const CUtensorMap* to) {
+__device__ int epi_warps(const Params& p, uint32_t base, uint8_t* gbase, uint32_t tmem, int wq,
+                         int lane, const CUtensorMap* to) {
   using C = Cfg<D>;
   const AttnArgs& a = p.a;
   const uint32_t bar = base + C::oBar;
@@ -516,11 +575,13 @@ __device__ int epi_warps(const Params& p, const Sched& sch, uint32_t base, uint8
   const bool leader = r == 0;
   auto all_ok = [](bool ok) { return __all_sync(0xffffffffu, ok); };
   int tc = 0;
-  for (int rd = 0, it; (it = item_at(rd)) < sch.count; ++rd) {
-    const Item x = sched_item(p, sch, it);
+  for (int rd = 0;; ++rd) {
+    Item x;
+    if (!next_item<D>(x, rd, bar, gbase, lane)) return kErrIFull;
+    if (x.nch < 0) break;
     if (x.nch == 0) continue;
     const int64_t bh = static_cast<int64_t>(x.b) * a.heads + x.h;
-    const int ob = tc % C::NOB, par = tc & 1;
+    const int par = tc & 1;
     if (!all_ok(mbar_wait(bar + 8 * (C::bXFull + par), (tc >> 1) & 1))) return kErrXFull;
     const float m0 = xs[((par * 2 + 0) * 2 + 0) * 128 + r], l0 = xs[((par * 2 + 0) * 2 + 1) * 128 + r];
     const float m1 = xs[((par * 2 + 1) * 2 + 0) * 128 + r], l1 = xs[((par * 2 + 1) * 2 + 1) * 128 + r];
@@ -539,8 +600,8 @@ __device__ int epi_warps(const Params& p, const Sched& sch, uint32_t base, uint8
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {  // 32 output columns at a time
       float o0[32], o1[32];
-      tmem_ld32(trow + C::tO(0, ob) + 32 * j, o0);
-      tmem_ld32(trow + C::tO(1, ob) + 32 * j, o1);
+      tmem_ld32(trow + C::tO(0) + 32 * j, o0);
+      tmem_ld32(trow + C::tO(1) + 32 * j, o1);
       tmem_wait_ld();
       reg_fence(o0);
       reg_fence(o1);
@@ -607,6 +668,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar + 8 * (C::bXFull + i), 256);
       mbar_init(bar + 8 * (C::bXFree + i), 128);
     }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(bar + 8 * (C::bIFull + i), 1);
+      mbar_init(bar + 8 * (C::bIFree + i), kTakers);
+    }
     mbar_init(bar + 8 * C::bVFix, 1);
     mbar_init(bar + 8 * C::bDone, 2);  // one commit per MMA-issuing thread
     fence_barrier_init();
@@ -634,16 +699,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   int err = 0;
   if (warp < 4) {
     regs_dec<C::kRegsCtl, kLaunchRegs>();
-    if (warp == 0 && lane == 0) err = producer<D>(p, sch, base, &tq, &tk);
-    if (warp == 1 && lane == 0) err = s_issuer<D>(p, sch, base, tmem);
-    if (warp == 2 && lane == 0) err = pv_issuer<D>(p, sch, base, tmem);
-    if (warp == 3) err = v_producer<D>(p, sch, base, gbase, lane, &tv);
+    if (warp == 0 && lane == 0) err = producer<D>(p, sch, base, gbase, &tq, &tk);
+    if (warp == 1 && lane == 0) err = s_issuer<D>(base, gbase, tmem);
+    if (warp == 2 && lane == 0) err = pv_issuer<D>(base, gbase, tmem);
+    if (warp == 3) err = v_producer<D>(p, base, gbase, lane, &tv);
   } else if (warp < 12) {
     regs_inc<C::kRegsSoft, kLaunchRegs>();
     err = softmax_warps<D>(p, sch, base, gbase, tmem, warp & 3, (warp - 4) >> 2, lane);
   } else {
     regs_dec<C::kRegsEpi, kLaunchRegs>();
-    err = epi_warps<D>(p, sch, base, gbase, tmem, warp & 3, lane, &to);
+    err = epi_warps<D>(p, base, gbase, tmem, warp & 3, lane, &to);
   }
   if (err) record_error(p.a.err, err);
 

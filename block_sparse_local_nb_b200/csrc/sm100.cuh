@@ -301,5 +301,19 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Position in a ring of N barriers and the parity of its current pass.
+template <int N>
+struct Ring {
+  int i = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int step = 1) {  // step <= N
+    i += step;
+    if (i >= N) {
+      i -= N;
+      ph ^= 1;
+    }
+  }
+};
+
 }  // namespace sm100
 }  // namespace nb
