@@ -61,7 +61,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
 struct Cfg {
-  static constexpr int NQ = D == 64 ? 2 : 1;   // Q tile buffers
+  static constexpr int NQ = 2;                 // Q tile buffers
   static constexpr int NKV = D == 64 ? 3 : 2;  // K chunk stages, and as many V chunk stages
   static constexpr int NSB = NKV;              // S buffers
   static constexpr int kQBytes = kRows * D * 2;
@@ -69,8 +69,8 @@ struct Cfg {
   static constexpr int oQ = 0;
   static constexpr int oK = oQ + NQ * kQBytes;
   static constexpr int oV = oK + NKV * kKBytes;
-  static constexpr int oStg = oV + NKV * kKBytes;  // output tile staging (D / 64 boxes)
-  static constexpr int oItem = oStg + kRows * D * 2;  // ring of items
+  static constexpr int oStg = oV + NKV * kKBytes;  // output staging, 64 columns of a tile
+  static constexpr int oItem = oStg + kSlab;  // ring of items
   static constexpr int oBar = oItem + kItems * 32;
   static_assert(oItem % 16 == 0, "items are read 16 bytes at once");
   // barrier indices ([S buffer][half] for P, [half][buffer] for O)
@@ -595,39 +595,41 @@ __device__ int epi_warps(const Params& p, uint32_t base, uint8_t* gbase, uint32_
     const float g0 = f0 * inv, g1 = f1 * inv;
     if (!all_ok(mbar_wait(bar + 8 * C::bOFull, tc & 1))) return kErrOFull;
     tc_fence_after();
-    if (leader) bulk_wait_read0();  // the previous tile's store is done with the staging
-    named_barrier(2, 128);
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) {  // 32 output columns at a time
-      float o0[32], o1[32];
-      tmem_ld32(trow + C::tO(0) + 32 * j, o0);
-      tmem_ld32(trow + C::tO(1) + 32 * j, o1);
-      tmem_wait_ld();
-      reg_fence(o0);
-      reg_fence(o1);
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        float w8[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          w8[i] = has ? fmaf(o0[8 * v + i], g0, o1[8 * v + i] * g1) : 0.f;
-        const int gc = 4 * j + v;  // 16-byte chunk index within the output row
-        *reinterpret_cast<uint4*>(stg + (gc >> 3) * kSlab + r * 128 + (((gc & 7) ^ (r & 7)) << 4)) =
-            make_uint4(pack_bf16(w8[0], w8[1]), pack_bf16(w8[2], w8[3]), pack_bf16(w8[4], w8[5]),
-                       pack_bf16(w8[6], w8[7]));
-      }
-    }
-    tc_fence_before();
-    mbar_arrive(bar + 8 * C::bOFree);
     const int q = x.tile * kRows + r;
     if (q < a.n && a.lse) a.lse[bh * a.n + q] = has ? (M + log2f(L)) * kLn2 : -INFINITY;
-    fence_proxy_async_smem();
-    named_barrier(1, 128);  // the whole tile is staged
-    if (leader) {
 #pragma unroll
-      for (int s = 0; s < D / 64; ++s)
-        tma_store_3d(to, base + C::oStg + s * kSlab, s * 64, x.tile * kRows, static_cast<int>(bh));
-      bulk_commit();
+    for (int s = 0; s < D / 64; ++s) {  // 64 output columns at a time
+      uint32_t w[32];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float o0[32], o1[32];
+        tmem_ld32(trow + C::tO(0) + 64 * s + 32 * j, o0);
+        tmem_ld32(trow + C::tO(1) + 64 * s + 32 * j, o1);
+        tmem_wait_ld();
+        reg_fence(o0);
+        reg_fence(o1);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          w[16 * j + i] = has ? pack_bf16(fmaf(o0[2 * i], g0, o1[2 * i] * g1),
+                                          fmaf(o0[2 * i + 1], g0, o1[2 * i + 1] * g1))
+                              : 0u;
+      }
+      if (s == D / 64 - 1) {  // the next tile's products may begin
+        tc_fence_before();
+        mbar_arrive(bar + 8 * C::bOFree);
+      }
+      if (leader) bulk_wait_read0();  // the store before is done with the staging
+      named_barrier(2, 128);
+#pragma unroll
+      for (int v = 0; v < 8; ++v)  // 16-byte pieces of the row, swizzled
+        *reinterpret_cast<uint4*>(stg + r * 128 + ((v ^ (r & 7)) << 4)) =
+            make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+      fence_proxy_async_smem();
+      named_barrier(1, 128);  // they are staged
+      if (leader) {
+        tma_store_3d(to, base + C::oStg, s * 64, x.tile * kRows, static_cast<int>(bh));
+        bulk_commit();
+      }
     }
     ++tc;
   }
