@@ -586,6 +586,15 @@ __device__ __forceinline__ uint64_t bit_range(int64_t lo, int64_t hi) {
   return b > a ? (~0ull >> (64 - (b - a))) << a : 0ull;
 }
 
+// The sign of byte b of x in every bit of the low half, of y in the high half.
+__device__ __forceinline__ uint32_t sign_halves(uint32_t x, uint32_t y, int b) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;"
+      : "=r"(r)
+      : "r"(x), "r"(y), "r"(0x8888u + 0x11u * b + 0x1100u * (4 + b)));
+  return r;
+}
+
 // P and dS of 64 columns of a chunk a warpgroup: half of every chunk (wide chunks),
 // or every second chunk.  Thread = lane r.
 template <int D, bool kDQ>
@@ -720,10 +729,12 @@ __device__ int grad_warps(const Params& p, uint32_t base, uint8_t* gbase,
                 ws[i] &= mw;
               }
             } else {
+              uint32_t top[8];  // bit 8 b + k of the word as the sign of byte b
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const uint32_t keep = ((mw >> (2 * i)) & 1u ? 0x0000ffffu : 0u) |
-                                      ((mw >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
+              for (int k = 0; k < 8; ++k) top[k] = mw << (7 - k);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {  // two bits to two half words of ones or zeros
+                const uint32_t keep = sign_halves(top[2 * i % 8], top[2 * i % 8 + 1], i / 4);
                 wp[i] &= keep;
                 ws[i] &= keep;
               }
