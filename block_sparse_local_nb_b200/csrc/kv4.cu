@@ -102,7 +102,11 @@ __device__ __forceinline__ void quantise16(const Row16& v, uint32_t (&w)[2], uin
   }
   lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
   hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
-  const float mid = bf16_below(__fadd_rd(0.5f * lo, 0.5f * hi));
+  // halved before the sum only where that could overflow: half of a subnormal is not
+  // exact, and two roundings down of the whole sum are one
+  const float mid = bf16_below(fmaxf(fabsf(lo), fabsf(hi)) < 0x1p126f
+                                   ? __fmul_rd(0.5f, __fadd_rd(lo, hi))
+                                   : __fadd_rd(__fmul_rd(0.5f, lo), __fmul_rd(0.5f, hi)));
   const float half = max_nan(__fsub_ru(hi, mid), __fsub_ru(mid, lo));
   if (!(half < __uint_as_float(0x7f800000u))) {  // NaN, infinity or overflow in the group
     param = 0x7fc07fc0u;

@@ -12,9 +12,10 @@ GROUP = 32
 
 
 def bf16_floor(x):
-    """Largest bf16 not above each finite fp64 value (normal range)."""
-    frac, exp = np.frexp(np.asarray(x, np.float64))
-    return np.ldexp(np.floor(frac * 256.0) / 256.0, exp)
+    """Largest bf16 not above each finite fp64 value (subnormal bf16 are multiples of 2^-133)."""
+    x = np.asarray(x, np.float64)
+    unit = np.ldexp(1.0, np.maximum(np.frexp(x)[1] - 8, -133))
+    return np.floor(x / unit) * unit
 
 
 def floor_ratio(x, mid, step):

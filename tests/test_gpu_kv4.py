@@ -154,6 +154,24 @@ def test_odd_groups(dtype):
     assert np.array_equal(v.cpu().numpy(), want, equal_nan=True)
 
 
+def test_subnormal_groups_are_exact():
+    """Extremes whose sum is odd in units of 2^-149: its half is no fp32 number, and a
+    midpoint just below a bf16 must not be rounded up to it."""
+    g = np.random.default_rng(8)
+    units = g.integers(-2 ** 18, 2 ** 18, (1, 1, 200, 64))
+    for t, base in enumerate((2 ** 17, 2 ** 16, 3 * 2 ** 16, -2 ** 16, -2 ** 17)):
+        units[0, 0, t] = base - g.integers(0, 2, 64)
+        units[0, 0, t, ::32], units[0, 0, t, 1::32] = base - 1, base
+    x = (units * 2.0 ** -149).astype(np.float32)
+    assert np.array_equal(x.astype(np.float64), units * 2.0 ** -149)
+    c = Cache(1, 1, 64, 7)
+    xd = torch.from_numpy(x).cuda()
+    c.write(xd, xd)
+    for y in c.read(200, torch.float32):
+        want = kv4.values(x.astype(np.float64))
+        assert np.array_equal(y.cpu().numpy().astype(np.float64), want)
+
+
 def test_every_border_is_exact():
     """Values on, just below and just above code borders of awkward steps."""
     g = np.random.default_rng(5)

@@ -239,6 +239,12 @@ def test_kv4_oracle_cells():
     assert (7.5 * below < np.maximum(hi - mid, mid - lo)).all() and (mid <= (lo + hi) / 2).all()
 
 
+def test_kv4_oracle_rounds_to_the_grid_of_bf16():
+    x = np.array([2.0 ** -133 * 1.75, -2.0 ** -133 * 0.5, 2.0 ** -126 * 1.999, 1.0 - 2.0 ** -30, -1.0 - 2.0 ** -30])
+    want = np.array([2.0 ** -133, -2.0 ** -133, 2.0 ** -126 * (2 - 2.0 ** -7), 1.0 - 2.0 ** -8, -1.0 - 2.0 ** -7])
+    assert np.array_equal(kv4.bf16_floor(x), want)
+
+
 def test_kv4_oracle_constant_groups_are_kept():
     x = np.repeat(np.array([0.0, -1.5, 3.140625])[:, None], 64, 1)
     assert (kv4.values(x) == x).all()
