@@ -6,10 +6,9 @@
 //   O = sum_j p_j v_j = sum_j (p_j s_jg)(c - 7.5) + sum_j p_j m_jg
 // so the codes themselves are the operands of warp matrix products (m16n8k16): no
 // row is ever dequantised in memory, and s and m enter in fp32 outside them.  A
-// nibble becomes bf16 by or-ing it into the mantissa of 128 (128 + c, exact).
+// nibble alone in a bf16 is a subnormal number, exactly (even_codes, below).
 //   Scores: rows = 16 tokens, columns = 8 query heads that share the key/value
-//   head; the products start from -135.5 sum(q_g), so 128 + 7.5 is off again in
-//   fp32.  sum_g m_jg sum(q_g) is one product more, over the bf16 midpoints and
+//   head; the products start from -7.5 sum(q_g).  sum_g m_jg sum(q_g) is one product more, over the bf16 midpoints and
 //   sum(q_g) cut into three bf16 parts (24 bits).
 //   Values: rows = 16 channels, columns = 8 heads; here the offset is subtracted
 //   from the codes before the product (exact in bf16), because the output sums
@@ -38,7 +37,7 @@ using namespace sm100;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kHeads = 16;  // query heads of one block (the rows of a product)
+constexpr int kHeads = 16;  // query heads of one block (two sets of a product's eight columns)
 constexpr int kMinShare = 4 * kWarps;  // pages: a share of fewer costs more than it gains
 constexpr float kTau = 8.0f;           // lazy-rescale threshold, log2 units
 constexpr float kLog2e = 1.4426950408889634f;
@@ -93,16 +92,6 @@ __device__ __forceinline__ Visible visible_pages(const Params& p, int b) {
   v.sink_pages = min(sp, v.page0);
   v.count = v.sink_pages + (v.len + kPage - 1) / kPage - v.page0;
   return v;
-}
-
-// d = a b + c (a row-major 16 x 16, b 16 x 8, bf16 in, fp32 out).
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1, const float (&c)[4]) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%10,%11,%12,%13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
-        "f"(c[2]), "f"(c[3]));
 }
 
 // A nibble alone in a bf16 is a number: the least significant bit of the exponent

@@ -6,8 +6,9 @@
 // dK and dV summed over the query heads that share a key/value head.
 //
 // Four launches on the caller's stream:
-//   rows   per query row -D and -lse log2(e) into the workspace (-inf past the
-//          length, so P is 0 there), and zeros for gradient tiles past it;
+//   rows   per query row -D (from its keys where they are few, see kFew) and
+//          -lse log2(e) into the workspace (-inf past the length, so P is 0
+//          there), and zeros for gradient tiles past it;
 //   main   <kDQ = false>: a 128-key tile of K and V stays, 64-query chunks of Q
 //          and dO stream past: S^T = K Q^T, dP^T = V dO^T (keys on the lanes),
 //          dV += P^T dO, dK += dS^T Q;
@@ -60,6 +61,9 @@ constexpr int kItems = 4;                 // items decoded ahead
 constexpr int kTakers = 14;               // arrivals that free one: 2 issuers, 8 + 4 warps
 
 struct Params {
+  const void* q;
+  const void* k;
+  const void* v;
   const void* o;
   const void* dout;
   const float* lse;
@@ -75,6 +79,7 @@ struct Params {
   int batch, heads, kv_heads, group, n, npad, ntiles, window, sinks;
   int s0, s1;    // parts of the first key tile, of another
   int items;     // of the main kernel
+  int term_blocks;  // of the row kernel: those of rows that see few keys
   int* taken;    // items taken so far by the CTAs of <kDQ = false>, <kDQ = true>
   float scale;
 };
@@ -951,23 +956,114 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// D of a row is rowsum(dO O), but O comes rounded to bf16, and the error that this
+// leaves in D is the same for all keys of the row: it falls with the root of their
+// number, and a row of a few keys has large gradients.  (Relative error of dQ and dK
+// at window 2: 0.0037, at lengths of 3: 0.010, where the rounding of dS and of the
+// result make 0.0024.)  Rows that see at most kFew keys, the first of a sequence or
+// all under a small window, therefore take D = sum_j P_j dP_j from their keys.
+constexpr int kFew = 32;
+// The rows of a sequence, from its first, that see few (npad: whole tiles of them).
+__host__ __device__ __forceinline__ int few_rows(int window, int sinks, int npad) {
+  return window <= kFew - sinks ? npad : kFew;
+}
+
+// -D of rows q0 .. q0 + 15 from their keys: a block of eight warps, each with eight keys
+// (there are hardly more than 64), so that the block takes little longer than those that
+// stream: the backward of 2 x 4 heads x 333 x 64 grows by 2 us, 4 with one warp for
+// all keys.  Warp products of 16 rows by 8 keys; a
+// lane's 16 bytes of a row are its operands of two products (which channels share a
+// step does not matter to the sum).
+template <int D>
+__device__ __forceinline__ void row_terms(const Params& p, int b, int h, int L, int q0) {
+  __shared__ float part[8][16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+  const int bh = b * p.heads + h, bkv = b * p.kv_heads + h / p.group;
+  auto piece = [&](const void* x, int head, int row) {  // the lane's first 16 bytes of a row
+    return reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) +
+                                          (static_cast<int64_t>(head) * p.n + min(row, L - 1)) * D) + t;
+  };
+  const uint4* q[2];
+  const uint4* g[2];
+  float nl[2], sum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = min(q0 + r + 8 * i, L - 1);
+    q[i] = piece(p.q, bh, row);
+    g[i] = piece(p.dout, bh, row);
+    nl[i] = -p.lse[static_cast<int64_t>(bh) * p.n + row] * kLog2e;
+  }
+  const float sl2 = p.scale * kLog2e;
+  const int k0 = q0 >= p.window ? q0 - p.window + 1 : 0;  // the first row's window
+  const int far = min(p.sinks, k0), far_steps = (far + 7) / 8;
+  const int steps = far_steps + (min(q0 + 16, L) - k0 + 7) / 8;
+#pragma unroll 1
+  for (int i = warp; i < steps; i += 8) {
+    const int first = i < far_steps ? 8 * i : k0 + 8 * (i - far_steps);
+    const uint4* k = piece(p.k, bkv, first + r);
+    const uint4* v = piece(p.v, bkv, first + r);
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, dp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int c = 0; c < D / 32; ++c) {  // 32 channels
+      auto step = [&](float (&acc)[4], const uint4* const (&a)[2], const uint4* b) {
+        const uint4 x = a[0][4 * c], y = a[1][4 * c], z = b[4 * c];
+        const uint32_t lo[4] = {x.x, y.x, x.y, y.y}, hi[4] = {x.z, y.z, x.w, y.w};
+        mma16816(acc, lo, z.x, z.y, acc);
+        mma16816(acc, hi, z.z, z.w, acc);
+      };
+      step(s, q, k);
+      step(dp, g, v);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int row = q0 + r + 8 * (e >> 1), key = first + 2 * t + (e & 1);
+      const bool seen = i < far_steps ? key < far
+                                      : key <= row && (row - key < p.window || key < p.sinks);
+      if (seen)
+        sum[e >> 1] = fmaf(ex2_approx(fmaf(s[e], sl2, nl[e >> 1])), dp[e], sum[e >> 1]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+    if (t == 0) part[warp][r + 8 * i] = sum[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < 16 && q0 + static_cast<int>(threadIdx.x) < L) {
+    float all = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) all += part[w][threadIdx.x];
+    p.nd[static_cast<int64_t>(bh) * p.npad + q0 + threadIdx.x] = -all;
+  }
+}
+
 // Row statistics (padded to whole tiles), zeros for the gradient rows of tiles
 // that lie past their sequence's length, and the counters of the main kernels.
+// The first blocks take the rows that see few keys, beside the others.
 // Block = kRowsPer rows of one (sequence, head); a thread has eight elements
 // (16 bytes) of kPer rows, all loaded before the first is used.
 constexpr int kPer = 4;
 template <int D>
 constexpr int kRowsPer = kPer * 256 / (D / 8);  // 64 or 128: divides a tile
 template <int D>
-__global__ void __launch_bounds__(256) sink_rows_kernel(const Params p) {
+__global__ void __launch_bounds__(256, 3) sink_rows_kernel(const Params p) {
   constexpr int TPR = D / 8, kStep = 256 / TPR;  // threads per row, rows at once
   pdl_trigger();
   pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x < 2) p.taken[threadIdx.x] = 0;
+  if (static_cast<int>(blockIdx.x) < p.term_blocks) {  // sixteen rows
+    const int per = few_rows(p.window, p.sinks, p.npad) / 16;
+    const int bh = static_cast<int>(blockIdx.x) / per;
+    const int f0 = (static_cast<int>(blockIdx.x) - bh * per) * 16;
+    const int b = bh / p.heads, L = length_of(p, b);
+    if (f0 < L) row_terms<D>(p, b, bh - b * p.heads, L, f0);
+    return;
+  }
   const int per = p.npad / kRowsPer<D>;  // blocks per (sequence, head)
-  const int bh = static_cast<int>(blockIdx.x / per);
-  const int q0 = static_cast<int>(blockIdx.x - static_cast<unsigned>(bh) * per) * kRowsPer<D> +
-                 threadIdx.x / TPR;
+  const int block = static_cast<int>(blockIdx.x) - p.term_blocks;
+  const int bh = block / per;
+  const int q0 = (block - bh * per) * kRowsPer<D> + threadIdx.x / TPR;
   const int part = threadIdx.x % TPR;
   const int b = bh / p.heads, h = bh - b * p.heads;
   const int L = length_of(p, b);
@@ -999,7 +1095,8 @@ __global__ void __launch_bounds__(256) sink_rows_kernel(const Params p) {
     for (int off = TPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
     if (part == 0) {
       const int64_t row = static_cast<int64_t>(bh) * p.npad + q;
-      p.nd[row] = -acc;  // stored negated: the main kernels form dP + (-D)
+      // stored negated: the main kernels form dP + (-D)
+      if (q >= L || q >= few_rows(p.window, p.sinks, p.npad)) p.nd[row] = -acc;
       p.nlse2[row] = q < L ? -p.lse[static_cast<int64_t>(bh) * p.n + q] * kLog2e : -INFINITY;
     }
     if (q < p.n && q / kRows * kRows >= L) {
@@ -1133,6 +1230,9 @@ cudaError_t run(const SinkArgs& a, cudaStream_t stream) {
   const Plan w = make_plan(a);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   Params p = {};
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
   p.o = a.o;
   p.dout = a.dout;
   p.lse = a.lse;
@@ -1158,8 +1258,11 @@ cudaError_t run(const SinkArgs& a, cudaStream_t stream) {
   p.s0 = w.s0;
   p.s1 = w.s1;
   p.scale = a.scale;
-  const int64_t blocks = static_cast<int64_t>(a.batch) * a.heads * (w.npad / kRowsPer<D>);
+  const int64_t hq = static_cast<int64_t>(a.batch) * a.heads;
+  const int64_t terms = hq * (few_rows(a.window, a.sinks, w.npad) / 16);
+  const int64_t blocks = terms + hq * (w.npad / kRowsPer<D>);
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  p.term_blocks = static_cast<int>(terms);
   cudaError_t e = launch_pdl(sink_rows_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
                              stream, p);
   if (e == cudaSuccess) e = launch_main<D, false>(a, p, stream);

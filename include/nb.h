@@ -321,8 +321,10 @@ NB_API nb_status nb_attn_sink_fwd(const void* q, const void* k, const void* v, v
 /*
  * nb_attn_sink_bwd - backward of nb_attn_sink_fwd from its stored log-sum-exp:
  * D = rowsum(dO O), dS = P (dO V^T - D), dV = P^T dO, dQ = dS K / sqrt(d),
- * dK = dS^T Q / sqrt(d); dK and dV are summed over the query heads that share a
- * key/value head.  All three gradients are deterministic.
+ * dK = dS^T Q / sqrt(d).  Rows that see at most 32 keys (the first 32, or all when
+ * window + sinks <= 32) take D = rowsum(P dO V^T), the same without O's rounding.
+ * dK and dV are summed over the query heads that share a key/value head.  All
+ * three gradients are deterministic.
  * q, k, v, o, lse, dout in : as nb_attn_bwd, with k, v of kv_heads heads.
  * dq         out: [batch, heads, n, d];  dk, dv out: [batch, kv_heads, n, d].
  *                 Rows past a sequence's length are written as 0.  The outputs

@@ -243,6 +243,25 @@ def test_autograd_on_strided_inputs():
         assert torch.equal(leaf.grad.transpose(1, 2), g)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads,kv_heads,n,window,sinks", [
+    (8, 8, 3, 3, 0), (4, 2, 40, 40, 1), (2, 1, 700, 2, 0), (2, 1, 700, 1, 4), (2, 2, 500, 31, 1)])
+def test_rows_of_few_keys_lose_nothing_to_the_rounded_output(heads, kv_heads, n, window, sinks, d):
+    """dQ and dK are off by two roundings, of dS and of the result.  One is uniform within
+    half a step of a value whose mantissa is spread over its logarithm: 2^-8 / sqrt(3)
+    times the root mean square of 1 / m, sqrt(3 / (8 ln 2)), is 1.66e-3 of the norm, two
+    independent ones 2.35e-3; the allowance for a finite sample is a fifth, 2.8e-3, and
+    two fifths for the few hundred elements of the shortest.  (With D from the rounded
+    O it is 3.7e-3 at window 2 and 1e-2 at n = 3.)"""
+    q, k, v, do = inputs(4, heads, kv_heads, n, d, n + window)
+    qd, kd, vd, dod = (x.cuda() for x in (q, k, v, do))
+    o, lse = run_fwd(qd, kd, vd, None, window, sinks)
+    grads = run_bwd(qd, kd, vd, o, dod, lse, None, window, sinks)
+    wants, _ = sink.bwd(*(f64(x) for x in (q, k, v, do)), window, sinks)
+    for g, w in zip(grads[:2], wants[:2]):
+        assert np.linalg.norm(f64(g) - w) <= (2.8e-3 if n > 3 else 3.3e-3) * np.linalg.norm(w)
+
+
 def test_gradients_against_differences():
     """Directional differences of the kernel's own fp32-summed loss.  The step h moves
     the bf16 inputs exactly (multiples of 2^-6 times +-1); the output's rounding enters the
