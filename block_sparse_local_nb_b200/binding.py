@@ -82,6 +82,25 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_entries = {}
+
+
+def _entry(name):
+    """The entry point `name` of the library, taking tensors, addresses or None as they
+    are: from the extension module, or through ctypes where that was not built."""
+    fn = _entries.get(name)
+    if fn is None:
+        plain = getattr(lib(), name)  # raises when the library is missing
+        try:
+            from . import _call
+
+            fn = getattr(_call, name)
+        except ImportError:
+            fn = lambda *a: plain(*(_ptr(x) for x in a))  # noqa: E731
+        _entries[name] = fn
+    return fn
+
+
 _raw_stream = None
 
 
@@ -216,8 +235,8 @@ def nb_batch_ceiling(offsets, batch, k=6) -> int:
 
 def nb_attn_sink_fwd(q, k, v, o, lse, lengths, batch, heads, kv_heads, n, d, window, sinks, dtype,
                      stream=None, check=True):
-    st = lib().nb_attn_sink_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(lengths),
-                                batch, heads, kv_heads, n, d, window, sinks, dtype, _stream(stream))
+    st = _entry("nb_attn_sink_fwd")(q, k, v, o, lse, lengths, batch, heads, kv_heads, n, d, window,
+                                    sinks, dtype, _stream(stream))
     if check:
         _check(st, "nb_attn_sink_fwd")
     return st
@@ -230,10 +249,9 @@ def attn_sink_bwd_workspace_size(batch, heads, kv_heads, n, d, window, sinks, dt
 
 def nb_attn_sink_bwd(q, k, v, o, dout, lse, lengths, dq, dk, dv, workspace, workspace_bytes, batch,
                      heads, kv_heads, n, d, window, sinks, dtype, stream=None, check=True):
-    st = lib().nb_attn_sink_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse),
-                                _ptr(lengths), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
-                                workspace_bytes, batch, heads, kv_heads, n, d, window, sinks, dtype,
-                                _stream(stream))
+    st = _entry("nb_attn_sink_bwd")(q, k, v, o, dout, lse, lengths, dq, dk, dv, workspace,
+                                    workspace_bytes, batch, heads, kv_heads, n, d, window, sinks,
+                                    dtype, _stream(stream))
     if check:
         _check(st, "nb_attn_sink_bwd")
     return st
@@ -246,9 +264,8 @@ def kv4_page_bytes(d) -> int:
 
 def nb_kv4_write(k, v, cache, block_table, starts, counts, batch, kv_heads, n, d, max_pages,
                  num_pages, dtype, stream=None, check=True):
-    st = lib().nb_kv4_write(_ptr(k), _ptr(v), _ptr(cache), _ptr(block_table), _ptr(starts),
-                            _ptr(counts), batch, kv_heads, n, d, max_pages, num_pages, dtype,
-                            _stream(stream))
+    st = _entry("nb_kv4_write")(k, v, cache, block_table, starts, counts, batch, kv_heads, n, d,
+                                max_pages, num_pages, dtype, _stream(stream))
     if check:
         _check(st, "nb_kv4_write")
     return st
@@ -256,9 +273,8 @@ def nb_kv4_write(k, v, cache, block_table, starts, counts, batch, kv_heads, n, d
 
 def nb_kv4_read(cache, block_table, starts, counts, k, v, batch, kv_heads, n, d, max_pages,
                 num_pages, dtype, stream=None, check=True):
-    st = lib().nb_kv4_read(_ptr(cache), _ptr(block_table), _ptr(starts), _ptr(counts), _ptr(k),
-                           _ptr(v), batch, kv_heads, n, d, max_pages, num_pages, dtype,
-                           _stream(stream))
+    st = _entry("nb_kv4_read")(cache, block_table, starts, counts, k, v, batch, kv_heads, n, d,
+                               max_pages, num_pages, dtype, _stream(stream))
     if check:
         _check(st, "nb_kv4_read")
     return st
@@ -273,10 +289,9 @@ def attn_kv4_decode_workspace_size(batch, heads, kv_heads, d, max_pages, window,
 def nb_attn_kv4_decode(q, cache, block_table, lengths, o, lse, workspace, workspace_bytes, batch,
                        heads, kv_heads, d, max_pages, num_pages, window, sinks, dtype, stream=None,
                        check=True):
-    st = lib().nb_attn_kv4_decode(_ptr(q), _ptr(cache), _ptr(block_table), _ptr(lengths), _ptr(o),
-                                  _ptr(lse), _ptr(workspace), workspace_bytes, batch, heads,
-                                  kv_heads, d, max_pages, num_pages, window, sinks, dtype,
-                                  _stream(stream))
+    st = _entry("nb_attn_kv4_decode")(q, cache, block_table, lengths, o, lse, workspace,
+                                      workspace_bytes, batch, heads, kv_heads, d, max_pages,
+                                      num_pages, window, sinks, dtype, _stream(stream))
     if check:
         _check(st, "nb_attn_kv4_decode")
     return st

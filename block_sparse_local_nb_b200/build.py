@@ -3,7 +3,8 @@
 Every ``csrc/*.cu`` is compiled for sm_100a only (``-gencode
 arch=compute_100a,code=sm_100a``) with line info, in parallel, and linked into
 one shared library with the CUDA runtime linked statically (the library needs
-the NVIDIA driver at run time, nothing else).  Usage::
+the NVIDIA driver at run time, nothing else).  ``csrc/pycall.cpp`` becomes the
+extension module ``_call`` beside it, which calls the library from Python.  Usage::
 
     python -m block_sparse_local_nb_b200.build [--verbose] [--ptxas-info]
 """
@@ -17,12 +18,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libnb_b200.so")
+CALL = os.path.join(PKG, "_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -47,6 +50,19 @@ def _compile(src: str, ptxas_info: bool) -> tuple[str, str]:
     return obj, res.stderr
 
 
+def _build_call() -> None:
+    """The extension module; its library is found beside it."""
+    tmp = CALL + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           "-fvisibility=hidden", "-I" + sysconfig.get_paths()["include"],
+           "-I" + os.path.join(ROOT, "include"), os.path.join(CSRC, "pycall.cpp"), "-o", tmp,
+           "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for pycall.cpp:\n{res.stderr}")
+    os.replace(tmp, CALL)
+
+
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -63,6 +79,7 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stderr}")
     os.replace(tmp, LIB)
+    _build_call()
     return LIB
 
 

@@ -8,8 +8,9 @@
 // row is ever dequantised in memory, and s and m enter in fp32 outside them.  A
 // nibble alone in a bf16 is a subnormal number, exactly (even_codes, below).
 //   Scores: rows = 16 tokens, columns = 8 query heads that share the key/value
-//   head; the products start from -7.5 sum(q_g).  sum_g m_jg sum(q_g) is one product more, over the bf16 midpoints and
-//   sum(q_g) cut into three bf16 parts (24 bits).
+//   head; the products start from -7.5 sum(q_g).  sum_g m_jg sum(q_g) is one
+//   product more, over the bf16 midpoints and sum(q_g) cut into three bf16 parts
+//   (24 bits).
 //   Values: rows = 16 channels, columns = 8 heads; here the offset is subtracted
 //   from the codes before the product (exact in bf16), because the output sums
 //   over many tokens and would cancel.  p s is rounded to bf16 and transposed

@@ -124,6 +124,47 @@ def test_layer_checks_arguments(built_lib):
 
 
 # ------------------------------------------------------------------- oracles
+@pytest.mark.parametrize("extension", [True, False])
+def test_binding_takes_tensors_addresses_and_none(built_lib, extension, monkeypatch):
+    """The new entry points through the extension module, and through ctypes where it is missing."""
+    import sys
+
+    import block_sparse_local_nb_b200 as nb
+    from block_sparse_local_nb_b200 import binding
+
+    monkeypatch.setattr(binding, "_entries", {})
+    if not extension:
+        monkeypatch.setitem(sys.modules, "block_sparse_local_nb_b200._call", None)
+        monkeypatch.delattr(sys.modules["block_sparse_local_nb_b200"], "_call", raising=False)
+    t = torch.empty(64)
+    kv = dict(stream=0, check=False)
+
+    def write(k=t, starts=None, d=64, n=1, cache=t):
+        return nb.nb_kv4_write(k, t, cache, t, starts, None, 1, 1, n, d, 4, 9, BF16, **kv)
+
+    assert write(d=63) == UNSUPPORTED and write(n=0) == NB_OK
+    assert write(k=None) == INVALID and write(cache=24) == MISALIGNED
+    assert write(starts=t[1:].data_ptr() + 1) == MISALIGNED
+    assert write(cache=2 ** 63 + 8) == MISALIGNED  # an address takes all 64 bits
+    with pytest.raises(nb.NbError):
+        nb.nb_kv4_read(t, t, None, None, t, t, 1, 1, 1, 32, 4, 9, BF16, stream=0)
+    with pytest.raises((TypeError, AttributeError)):
+        write(k="a tensor")
+    with pytest.raises((TypeError, AttributeError)):
+        write(d=64.0)
+    assert nb.nb_attn_sink_fwd(t, t, t, t, None, None, 1, 2, 1, 8, 96, 4, 0, BF16, **kv) == UNSUPPORTED
+    assert nb.nb_attn_sink_bwd(t, t, t, t, t, t, None, t, t, t, 256, 2 ** 40, 1, 3, 2, 8, 64, 4, 0,
+                               BF16, **kv) == INVALID
+    assert nb.nb_attn_kv4_decode(t, t, t, None, t, None, None, 0, 1, 2, 1, 64, 4, 9, 0, 0, BF16,
+                                 **kv) == INVALID
+    if extension:
+        assert isinstance(binding._entries["nb_kv4_write"], type(len))
+        with pytest.raises(OverflowError):
+            write(n=2 ** 31)
+        with pytest.raises(TypeError):
+            binding._entry("nb_kv4_write")(t, t)
+
+
 def draw(batch, heads, kv_heads, n, d, seed=0):
     g = np.random.default_rng(seed)
     return (g.standard_normal((batch, heads, n, d)), g.standard_normal((batch, kv_heads, n, d)),
