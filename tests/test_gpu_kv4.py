@@ -225,7 +225,8 @@ def test_decode(heads, kv_heads, lengths, window, sinks, d):
 
 @pytest.mark.parametrize("d,batch,kv_heads,heads,n,window,sinks",
                          [(64, 1, 1, 4, 20000, 1 << 30, 0), (128, 3, 2, 2, 9001, 4096, 4),
-                          (128, 1, 2, 16, 5000, 1 << 30, 0)])
+                          (128, 1, 2, 16, 5000, 1 << 30, 0), (128, 1, 2, 16, 1000, 1 << 30, 0),
+                          (64, 2, 1, 9, 700, 400, 33), (128, 40, 1, 3, 1500, 1 << 30, 0)])
 def test_decode_long_in_shares(d, batch, kv_heads, heads, n, window, sinks):
     """Long sequences are cut into shares that are joined; twice gives the same bits."""
     pages = -(-n // PAGE) + 2
@@ -233,9 +234,9 @@ def test_decode_long_in_shares(d, batch, kv_heads, heads, n, window, sinks):
     k, v = (rows((batch, kv_heads, n, d), s, torch.bfloat16) for s in (1, 2))
     lengths = [n - 37 * b for b in range(batch)]
     c.write(k.cuda(), v.cuda(), None, i32(lengths))
-    # one row with 40 shares goes through the workspace, the others join in clusters
+    # rows of many shares go through the workspace, the others join in clusters
     assert bool(nb.attn_kv4_decode_workspace_size(batch, heads, kv_heads, d, pages, window, sinks,
-                                                  nb.NB_BF16)) == (n == 20000)
+                                                  nb.NB_BF16)) == (n >= 5000)
     q = torch.randn(batch, heads, d, generator=torch.Generator().manual_seed(3)).bfloat16()
     kq, vq = kv4.values(k.double().numpy()), kv4.values(v.double().numpy())
     a = check_decode(c, q, kq, vq, lengths, window, sinks)
@@ -262,7 +263,7 @@ def test_decode_of_queries_and_keys_of_any_size(up, down, d):
     check_decode(c, q, kv4.values(k.double().numpy()), kv4.values(v.double().numpy()), lengths, 100, 3)
 
 
-@pytest.mark.parametrize("n", [1, 100, 3000, 20000])  # one warp, a block, a cluster, the workspace
+@pytest.mark.parametrize("n", [1, 100, 1000, 3000, 20000])  # one warp, a block, a cluster, the workspace
 def test_decode_of_what_is_not_a_number(n):
     """A key that is no number, where it is visible, makes its head's outputs none; a
     value makes its group of channels none; where they are hidden nothing changes."""
