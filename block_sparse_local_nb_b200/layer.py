@@ -130,7 +130,11 @@ class SinkAttention(torch.autograd.Function):
     """O = softmax(Q K^T / sqrt(d)) V where query q sees key k when k <= q,
     k < lengths[b] and (q - k < window or k < sinks), with its backward.  q is
     [batch, heads, n, d], k and v [batch, kv_heads, n, d]; query head h reads
-    key/value head h // (heads // kv_heads)."""
+    key/value head h // (heads // kv_heads).
+
+    A pass may be captured into a graph; its backward with ``torch.autograd.grad``, or
+    with leaves that no earlier graph still holds (torch adds a leaf's gradient on
+    the stream of the graph that lives, outside of the capture)."""
 
     @staticmethod
     def forward(ctx, q, k, v, lengths, window: int, sinks: int = 0):

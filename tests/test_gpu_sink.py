@@ -209,6 +209,36 @@ def test_other_stream_and_graph_replay():
             assert all(torch.equal(x, y) for x, y in zip(want, first))
 
 
+def test_layer_captured_with_its_gradients():
+    """The layer's function and its backward in one graph, replayed on new inputs."""
+    from block_sparse_local_nb_b200.layer import sink_attention
+
+    q, k, v, do = (x.cuda() for x in inputs(2, 4, 1, 300, 64, 21))
+    lengths = i32([300, 77])
+    leaves = [x.requires_grad_(True) for x in (q, k, v)]
+
+    def step():
+        o = sink_attention(*leaves, lengths, 90, 2)
+        return [o.detach(), *torch.autograd.grad(o, leaves, do)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for x, y in zip((q, k, v, do), inputs(2, 4, 1, 300, 64, 22)):
+        with torch.no_grad():
+            x.copy_(y)
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [x.clone() for x in held]
+    for x, y in zip(got, step()):
+        assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("n,window", [(1, 1), (300, 50), (1000, 400)])
 def test_what_is_not_a_number_reaches_the_rows_that_see_it(n, window, d):
