@@ -9,6 +9,7 @@
 
 #include "../../include/nb.h"
 #include "nb_internal.h"
+#include "serving.cuh"
 
 namespace {
 

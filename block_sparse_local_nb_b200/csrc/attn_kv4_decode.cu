@@ -27,8 +27,7 @@
 #include <type_traits>
 
 #include "kv4.cuh"
-#include "nb_internal.h"
-#include "sm100.cuh"
+#include "serving.cuh"
 
 namespace nb {
 namespace {

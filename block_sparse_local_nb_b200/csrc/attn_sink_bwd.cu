@@ -43,8 +43,7 @@
 // and TMA tensor stores.  Every wait is bounded (sm100.cuh).
 #include <math.h>
 
-#include "nb_internal.h"
-#include "sm100.cuh"
+#include "serving.cuh"
 
 namespace nb {
 namespace {

@@ -38,9 +38,8 @@
 // and tears down (frees TMEM) instead of hanging.
 #include <math.h>
 
-#include "nb_internal.h"
 #include "schedule.cuh"
-#include "sm100.cuh"
+#include "serving.cuh"
 
 namespace nb {
 namespace {

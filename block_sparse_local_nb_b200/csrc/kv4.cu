@@ -23,8 +23,7 @@
 #include <cuda_bf16.h>
 
 #include "kv4.cuh"
-#include "nb_internal.h"
-#include "sm100.cuh"
+#include "serving.cuh"
 
 namespace nb {
 namespace {

@@ -30,49 +30,6 @@ struct AttnArgs {
   bool causal;        // causal band: key blocks i - R..i of query block i, keys k <= q
 };
 
-// Arguments of an attention call with a window and sinks, validated on the host.
-struct SinkArgs {
-  const void* q;
-  const void* k;
-  const void* v;
-  const void* o;      // forward: output; backward: input
-  const void* dout;   // backward only
-  float* lse;         // forward: output (may be null); backward: input
-  const int32_t* lengths;  // may be null = all full
-  void* dq;
-  void* dk;
-  void* dv;
-  void* workspace;
-  int* err;
-  int batch, heads, kv_heads, n, d, window, sinks;
-  float scale;        // 1/sqrt(d)
-};
-
-// Arguments of a write to or a read from the 4-bit cache.
-struct Kv4Args {
-  void* k;  // write: input; read: output
-  void* v;
-  void* cache;
-  const int32_t* table;
-  const int32_t* starts;  // may be null = 0
-  const int32_t* counts;  // may be null = n
-  int* err;
-  int batch, kv_heads, n, d, max_pages, num_pages;
-  bool f32;
-};
-
-struct Kv4DecodeArgs {
-  const void* q;
-  const void* cache;
-  const int32_t* table;
-  const int32_t* lengths;
-  void* o;
-  float* lse;
-  void* workspace;
-  int* err;
-  int batch, heads, kv_heads, d, max_pages, num_pages, window, sinks;
-};
-
 size_t bwd_workspace_bytes(int64_t rows, int d);
 __host__ __device__ inline int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
@@ -116,27 +73,6 @@ __device__ __forceinline__ void pdl_trigger() {
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// The same with the grid's blocks in clusters of `cluster` along x (1: none).
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                               cudaStream_t stream, int cluster, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t stream, const Args&... args) {
@@ -167,12 +103,5 @@ cudaError_t launch_tokenize_batch(const uint8_t* seqs, const int64_t* offsets, i
 cudaError_t launch_attn_fwd_f32(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_fwd_bf16_tc(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_bwd_bf16(const AttnArgs& a, cudaStream_t stream);
-cudaError_t launch_attn_sink_fwd(const SinkArgs& a, cudaStream_t stream);
-size_t sink_bwd_workspace_bytes(const SinkArgs& a);
-cudaError_t launch_attn_sink_bwd(const SinkArgs& a, cudaStream_t stream);
-int kv4_page_bytes(int d);  // d = 64 or 128
-cudaError_t launch_kv4(const Kv4Args& a, bool write, cudaStream_t stream);
-size_t kv4_decode_workspace_bytes(const Kv4DecodeArgs& a);
-cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t stream);
 
 }  // namespace nb

@@ -301,29 +301,5 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Position in a ring of N barriers and the parity of its current pass.
-template <int N>
-struct Ring {
-  int i = 0;
-  uint32_t ph = 0;
-  __device__ __forceinline__ void next(int step = 1) {  // step <= N
-    i += step;
-    if (i >= N) {
-      i -= N;
-      ph ^= 1;
-    }
-  }
-};
-
-// d = a b + c (a row-major 16 x 16, b 16 x 8, bf16 in, fp32 out).
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1, const float (&c)[4]) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%10,%11,%12,%13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
-        "f"(c[2]), "f"(c[3]));
-}
-
 }  // namespace sm100
 }  // namespace nb

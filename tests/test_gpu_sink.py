@@ -275,7 +275,8 @@ def test_autograd_on_strided_inputs():
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("heads,kv_heads,n,window,sinks", [
-    (8, 8, 3, 3, 0), (4, 2, 40, 40, 1), (2, 1, 700, 2, 0), (2, 1, 700, 1, 4), (2, 2, 500, 31, 1)])
+    (8, 8, 3, 3, 0), (4, 2, 40, 40, 1), (2, 1, 700, 2, 0), (2, 1, 700, 1, 4), (2, 2, 500, 31, 1),
+    (3, 1, 300, 2, 30)])
 def test_rows_of_few_keys_lose_nothing_to_the_rounded_output(heads, kv_heads, n, window, sinks, d):
     """dQ and dK are off by two roundings, of dS and of the result.  One is uniform within
     half a step of a value whose mantissa is spread over its logarithm: 2^-8 / sqrt(3)
