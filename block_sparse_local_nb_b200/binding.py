@@ -136,7 +136,8 @@ def _check(status: int, what: str):
 
 
 def nb_kernel_error(clear: bool = True) -> int:
-    """Synchronise the device and return the first recorded kernel wait-timeout code (0 = none)."""
+    """Synchronise the device and return the first recorded code (0 = none): NB_KERR_WAIT |
+    site of a wait that ran out, else NB_KERR_KV4_* of a token that is not mapped."""
     code = ctypes.c_int(0)
     _check(lib().nb_kernel_error(ctypes.byref(code), 1 if clear else 0), "nb_kernel_error")
     return code.value

@@ -19,7 +19,8 @@ int g_device_ok[kMaxDevices];
 
 // Device word where kernels record the first wait-timeout code (0 = none),
 // and its device address per device (looked up once).
-__device__ int g_kernel_error;
+// the site of the first wait that ran out, and the first NB_KERR_KV4_* code
+__device__ int g_kernel_error[2];
 std::mutex g_err_mutex;
 int* g_err_addr[kMaxDevices];
 
@@ -36,6 +37,10 @@ int* error_word() {
     g_err_addr[dev] = static_cast<int*>(p);
   }
   return g_err_addr[dev];
+}
+int* skip_word() {
+  int* w = error_word();
+  return w ? w + 1 : nullptr;
 }
 
 nb_status check_device() {
@@ -191,7 +196,7 @@ nb_status kv4_rows(const void* k, const void* v, const void* cache, const int32_
   st = check_device();
   if (st != NB_OK) return st;
   nb::Kv4Args a = {const_cast<void*>(k), const_cast<void*>(v), const_cast<void*>(cache), table,
-                   starts, counts, error_word(), batch, kv_heads, n, d, max_pages, num_pages,
+                   starts, counts, skip_word(), batch, kv_heads, n, d, max_pages, num_pages,
                    dtype == NB_F32};
   const cudaError_t e = nb::launch_kv4(a, write, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? NB_OK : NB_ERR_CUDA;
@@ -254,8 +259,12 @@ nb_status nb_kernel_error(int* code, int clear) {
   int* w = error_word();
   if (!w) return NB_ERR_CUDA;
   if (cudaDeviceSynchronize() != cudaSuccess) return NB_ERR_CUDA;
-  if (cudaMemcpy(code, w, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return NB_ERR_CUDA;
-  if (clear && *code != 0 && cudaMemset(w, 0, sizeof(int)) != cudaSuccess) return NB_ERR_CUDA;
+  int words[2];
+  if (cudaMemcpy(words, w, sizeof(words), cudaMemcpyDeviceToHost) != cudaSuccess) return NB_ERR_CUDA;
+  const nb::KernelReport r = nb::kernel_report(words);
+  *code = r.code;
+  if (clear && r.code != 0 && cudaMemset(w + r.word, 0, sizeof(int)) != cudaSuccess)
+    return NB_ERR_CUDA;
   return NB_OK;
 }
 
@@ -434,8 +443,8 @@ nb_status nb_attn_kv4_decode(const void* q, const void* cache, const int32_t* bl
   if (!aligned16(q) || !aligned16(o) || !aligned16(cache) || !aligned4(block_table) ||
       !aligned4(lengths) || !aligned4(lse))
     return NB_ERR_MISALIGNED;
-  nb::Kv4DecodeArgs a = {q, cache, block_table, lengths, o, lse, workspace, nullptr, batch, heads,
-                         kv_heads, d, max_pages, num_pages, window, sinks};
+  nb::Kv4DecodeArgs a = {q, cache, block_table, lengths, o, lse, workspace, nullptr, nullptr, batch,
+                         heads, kv_heads, d, max_pages, num_pages, window, sinks};
   const size_t need = nb::kv4_decode_workspace_bytes(a);
   if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
                    workspace_bytes < need))
@@ -443,6 +452,7 @@ nb_status nb_attn_kv4_decode(const void* q, const void* cache, const int32_t* bl
   st = check_device();
   if (st != NB_OK) return st;
   a.err = error_word();
+  a.skip = skip_word();
   const cudaError_t e = nb::launch_kv4_decode(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? NB_OK : NB_ERR_CUDA;
 }

@@ -66,7 +66,8 @@ struct Params {
   const int32_t* lengths;  // null: every sequence is max_pages pages long
   float* part;             // splits > 1: [batch][heads][splits][d], then (m, l) pairs
   float2* part_ml;
-  int* err;
+  int* err;   // a wait that ran out
+  int* skip;  // a page that is not mapped
   int heads, group, head_blocks, splits, window, sinks;
   bool cluster;  // the shares of a row are one cluster
   float sl2;  // log2(e) / sqrt(d)
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
                   p.pool.base + (static_cast<int64_t>(id) * p.pool.kv_heads + kvh) * P::kBytes,
                   P::kBytes, bar + 8 * st);
       } else {  // a page outside the pool is reported and not seen
-        record_error(p.err, kErrDecodePage);
+        record_error(p.skip, kErrDecodePage);
         mbar_arrive(bar + 8 * st);
       }
     }
@@ -719,6 +720,7 @@ cudaError_t run(const Kv4DecodeArgs& a, cudaStream_t stream) {
   p.lse = a.lse;
   p.lengths = a.lengths;
   p.err = a.err;
+  p.skip = a.skip;
   p.heads = a.heads;
   p.group = a.heads / a.kv_heads;
   p.head_blocks = (p.group + kHeads - 1) / kHeads;

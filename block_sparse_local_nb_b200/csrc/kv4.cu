@@ -195,7 +195,7 @@ constexpr int kRows = kThreads / (D / 16);  // tokens of a block
 template <int D, bool kF32>
 __global__ void __launch_bounds__(kThreads)
     kv4_write_kernel(const void* k, const void* v, Pool pool, const int32_t* starts,
-                     const int32_t* counts, int n, int* err) {
+                     const int32_t* counts, int n, int* skip) {
   constexpr int kLanes = D / 16;  // threads per row
   pdl_trigger();
   pdl_wait();
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t at =
       ((static_cast<int64_t>(b) * pool.kv_heads + h) * n + min(t, count - 1)) * D + 16 * j;
   const Row16 kr = load16<kF32>(k, at), vr = load16<kF32>(v, at);
-  if (!s.page && t < count && j == 0) sm100::record_error(err, kErrWriteSlot);
+  if (!s.page && t < count && j == 0) sm100::record_error(skip, kErrWriteSlot);
   uint32_t kw[2], vw[2], kpar, vpar;
   quantise16(kr, kw, kpar);
   quantise16(vr, vw, vpar);
@@ -274,7 +274,7 @@ __device__ __forceinline__ void store8(void* p, int64_t at, uint32_t w, uint32_t
 template <int D, bool kF32>
 __global__ void __launch_bounds__(kThreads)
     kv4_read_kernel(void* k, void* v, Pool pool, const int32_t* starts, const int32_t* counts,
-                    int n, int* err) {
+                    int n, int* skip) {
   using P = Page<D>;
   constexpr int NG = P::kGroups;
   pdl_trigger();
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads)
       load(kpar, s.page + P::oKPar + s.token * P::kParRow);
       load(vpar, s.page + P::oVPar + s.token * P::kParRow);
     } else if (t < count && j == 0) {
-      sm100::record_error(err, kErrReadSlot);
+      sm100::record_error(skip, kErrReadSlot);
     }
   }
   // The words of chunks 2 j, 2 j + 1 (chunk bits j1 j0 e, word bit e its own), nibble
@@ -342,9 +342,9 @@ cudaError_t run(const Kv4Args& a, bool write, cudaStream_t stream) {
   if (write)
     return launch_pdl(kv4_write_kernel<D, kF32>, grid, block, 0, stream,
                       static_cast<const void*>(a.k), static_cast<const void*>(a.v), make_pool(a),
-                      a.starts, a.counts, a.n, a.err);
+                      a.starts, a.counts, a.n, a.skip);
   return launch_pdl(kv4_read_kernel<D, kF32>, grid, block, 0, stream, a.k, a.v, make_pool(a),
-                    a.starts, a.counts, a.n, a.err);
+                    a.starts, a.counts, a.n, a.skip);
 }
 
 }  // namespace

@@ -64,9 +64,9 @@ struct Pool {
   int max_pages, num_pages, kv_heads;
 };
 
-// error codes of slots that the table does not map into the pool, and of a wait
+// codes of slots that the table does not map into the pool, and the site of a wait
 enum : int { kErrWriteSlot = NB_KERR_KV4_WRITE, kErrReadSlot = NB_KERR_KV4_READ,
-             kErrDecodePage = NB_KERR_KV4_DECODE, kErrDecodeWait = 0x54 };
+             kErrDecodePage = NB_KERR_KV4_DECODE, kErrDecodeWait = 0xa1 };
 
 }  // namespace kv4
 }  // namespace nb

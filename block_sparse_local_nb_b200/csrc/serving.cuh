@@ -33,7 +33,7 @@ struct Kv4Args {
   const int32_t* table;
   const int32_t* starts;  // may be null = 0
   const int32_t* counts;  // may be null = n
-  int* err;
+  int* skip;  // first token that was not mapped
   int batch, kv_heads, n, d, max_pages, num_pages;
   bool f32;
 };
@@ -46,9 +46,20 @@ struct Kv4DecodeArgs {
   void* o;
   float* lse;
   void* workspace;
-  int* err;
+  int* err;   // first wait that ran out
+  int* skip;  // first page that was not mapped
   int batch, heads, kv_heads, d, max_pages, num_pages, window, sinks;
 };
+
+// What nb_kernel_error makes of the two device words, the site of a wait that ran out and
+// a NB_KERR_KV4_* code: the first of them that is set, and which.
+struct KernelReport {
+  int code, word;
+};
+inline KernelReport kernel_report(const int (&words)[2]) {
+  if (words[0] != 0) return {NB_KERR_WAIT | words[0], 0};
+  return {words[1], 1};
+}
 
 // launch_pdl with the grid's blocks in clusters of `cluster` along x (1: none).
 template <typename... KArgs, typename... Args>

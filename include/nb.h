@@ -87,14 +87,17 @@ NB_API int nb_abi_version(void);
 
 /*
  * nb_kernel_error - report whether a kernel gave up waiting.  Every wait inside
- * the tensor-core kernels is bounded (2 s); a kernel that runs out records a
+ * the kernels is bounded (2 s); a kernel that runs out records a
  * non-zero site code in a device word, frees its tensor memory and returns, so
- * the context stays usable (its outputs are then undefined).  The calls on the
- * 4-bit cache record NB_KERR_* there for a token that the block table does not
- * map.  This call
+ * the context stays usable (its outputs are then undefined): NB_KERR_WAIT | site.
+ * The calls on the 4-bit cache record NB_KERR_KV4_*, without that bit, for a token
+ * that the block table does not map; their other outputs are defined.  Either
+ * kind keeps its first code, in a word of its own.  This call
  * synchronises the current device, stores the recorded code (0 = none) in
- * *code and, when `clear` is non-zero, resets it.
+ * *code and, when `clear` is non-zero, resets it.  A wait's code is reported first,
+ * and the other kind's by the call after the one that reset it.
  */
+#define NB_KERR_WAIT 0x100      /* a wait ran out: outputs are undefined */
 #define NB_KERR_KV4_WRITE 0x51  /* nb_kv4_write skipped a token */
 #define NB_KERR_KV4_READ 0x52   /* nb_kv4_read wrote 0 for a token */
 #define NB_KERR_KV4_DECODE 0x53 /* nb_attn_kv4_decode did not see a page */
