@@ -491,12 +491,12 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
     }
   };
 
-  bool timed_out = false;
   int st = 0, phase = 0;
   for (int i = 0; i < mine; ++i) {
     if (!__all_sync(0xffffffffu, mbar_wait(bar + 8 * st, phase))) {
       if (lane == 0) record_error(p.err, kErrDecodeWait);
-      timed_out = true;
+      // copies still in flight must land before the ring is reused and the block exits
+      drain_pages<C::kStages>(i, mine, [&](int s, uint32_t ph) { mbar_wait(bar + 8 * s, ph); });
       break;
     }
     if (ok[st]) {
@@ -513,9 +513,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
       st = 0;
       phase ^= 1;
     }
-  }
-  if (timed_out) {  // copies still in flight must land before the block may exit
-    for (int i = 0; i < C::kStages; ++i) mbar_wait(bar + 8 * i, 0);
   }
 
   __syncthreads();  // every warp is done with its ring

@@ -64,6 +64,16 @@ struct Pool {
   int max_pages, num_pages, kv_heads;
 };
 
+// A warp brings the `count` pages of its share through N stages, page i into stage i mod N:
+// N pages at the start, and page i + N once page i has been used.  When the wait for page i
+// gives up, pages i .. i + N - 1 are on their way: calls wait(stage, parity) for each, with
+// the parity of the pass that the stage's barrier is in (i / N passes are complete).
+template <int N, class Wait>
+__host__ __device__ __forceinline__ void drain_pages(int i, int count, Wait&& wait) {
+  const int end = count - i < N ? count : i + N;
+  for (; i < end; ++i) wait(i % N, static_cast<uint32_t>(i / N) & 1u);
+}
+
 // codes of slots that the table does not map into the pool, and the site of a wait
 enum : int { kErrWriteSlot = NB_KERR_KV4_WRITE, kErrReadSlot = NB_KERR_KV4_READ,
              kErrDecodePage = NB_KERR_KV4_DECODE, kErrDecodeWait = 0xa1 };
