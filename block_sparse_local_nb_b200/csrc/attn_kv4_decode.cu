@@ -123,6 +123,8 @@ __device__ __forceinline__ uint32_t centred_odd(uint32_t w) {
   return centred(odd_codes(w), 0xbff0bff0u);  // -7.5 / 4
 }
 
+constexpr int kBigQuery = 112, kBigUnit = 16;  // (see the query operand)
+
 __device__ __forceinline__ float pow2(int e) {  // -126 <= e <= 127
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
@@ -257,10 +259,13 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
   // pairs of a code word.  With 2^e the largest power of two in the head's row, the
   // operands are q 2^(126 - e) for the even codes (c 2^-133) and a sixteenth of it for
   // the odd ones (c 2^-129): the products are q c 2^(-7 - e), and the scores carry that
-  // factor until sl2 takes it out.  off_g = -7.5 sum(q_g) of heads 2 t, 2 t + 1.
+  // factor until sl2 takes it out.  That takes up to 2^134, which is no float: heads with
+  // e > kBigQuery have kBigUnit of it multiplied into their scores first.
+  // off_g = -7.5 sum(q_g) of heads 2 t, 2 t + 1.
   constexpr int NP = NG / 2;
   uint32_t qb[kSets][2 * NG][2], qm[kSets][2];
   float off[kSets][NG][2], sl2[kSets][2];
+  uint32_t big = 0;  // bit 2 hs + j: such a head
 #pragma unroll
   for (int hs = 0; hs < kSets; ++hs) {
     const int head = r + 8 * hs;
@@ -285,9 +290,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
     const uint32_t down = down1 | down1 << 16;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int n = 7 + __shfl_sync(0xffffffffu, e, 8 * t + 4 * j);
-      // beyond the largest float no two different scores have comparable weights
-      sl2[hs][j] = fminf(p.sl2 * pow2(n / 2) * pow2(n - n / 2), 3.402823466e38f);
+      const int ej = __shfl_sync(0xffffffffu, e, 8 * t + 4 * j);
+      if (ej > kBigQuery) big |= 1u << (2 * hs + j);
+      const int n = 7 + ej - (ej > kBigQuery ? kBigUnit : 0);
+      sl2[hs][j] = p.sl2 * pow2(n / 2) * pow2(n - n / 2);
     }
     float qs[NG];
 #pragma unroll
@@ -324,6 +330,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
     qm[hs][0] = part == 0 ? parts[0] : part == 1 ? parts[1] : part == 2 ? parts[2] : 0u;
     qm[hs][1] = NP == 2 && part == 0 ? parts[2] : 0u;
   }
+
+  const bool any_big = __any_sync(0xffffffffu, big != 0);
 
   // of heads 2 t + j (+ 8 hs): the maximum in use, this lane's sums of p and of p m_g
   // (its tokens are 16 i + r, + 8), and the output at channels 16 i + r, + 8
@@ -385,6 +393,13 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D, kSets)) kv4_decode_
           s[hs][mt][2] = fmaf(st1, acc[2], s[hs][mt][2]);
           s[hs][mt][3] = fmaf(st1, acc[3], s[hs][mt][3]);
         }
+      }
+      if (any_big) {
+#pragma unroll
+        for (int hs = 0; hs < kSets; ++hs)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[hs][mt][e] *= big >> (2 * hs + (e & 1)) & 1 ? pow2(kBigUnit) : 1.f;
       }
       if (!kWhole) {
 #pragma unroll
