@@ -1,4 +1,6 @@
-"""Thin ctypes binding of the C ABI in ``include/nb.h`` (argument marshalling only).
+"""Thin binding of the C ABI in ``include/nb.h`` (argument marshalling only): through
+ctypes, and for the entry points whose kernels take a few microseconds through the
+extension module ``_call`` where it was built.
 
 Functions carry the C names and accept torch tensors (their ``data_ptr()`` is
 passed) or raw integer addresses.  Every step of the computation runs in
@@ -87,15 +89,19 @@ _entries = {}
 
 def _entry(name):
     """The entry point `name` of the library, taking tensors, addresses or None as they
-    are: from the extension module, or through ctypes where that was not built."""
+    are: from the extension module, or through ctypes where that was not built for
+    this library."""
     fn = _entries.get(name)
     if fn is None:
         plain = getattr(lib(), name)  # raises when the library is missing
         try:
             from . import _call
 
-            fn = getattr(_call, name)
-        except ImportError:
+            if _call.abi_version == lib().nb_abi_version():
+                fn = getattr(_call, name)
+        except (ImportError, AttributeError):
+            pass
+        if fn is None:
             fn = lambda *a: plain(*(_ptr(x) for x in a))  # noqa: E731
         _entries[name] = fn
     return fn

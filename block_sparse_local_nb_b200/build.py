@@ -4,7 +4,8 @@ Every ``csrc/*.cu`` is compiled for sm_100a only (``-gencode
 arch=compute_100a,code=sm_100a``) with line info, in parallel, and linked into
 one shared library with the CUDA runtime linked statically (the library needs
 the NVIDIA driver at run time, nothing else).  ``csrc/pycall.cpp`` becomes the
-extension module ``_call`` beside it, which calls the library from Python.  Usage::
+extension module ``_call`` beside it, which calls the library from Python; where it
+cannot be compiled (no g++ or Python headers) the binding calls through ctypes.  Usage::
 
     python -m block_sparse_local_nb_b200.build [--verbose] [--ptxas-info]
 """
@@ -19,6 +20,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -57,7 +59,10 @@ def _build_call() -> None:
            "-fvisibility=hidden", "-I" + sysconfig.get_paths()["include"],
            "-I" + os.path.join(ROOT, "include"), os.path.join(CSRC, "pycall.cpp"), "-o", tmp,
            "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        res = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"g++ did not run: {e}") from e
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed for pycall.cpp:\n{res.stderr}")
     os.replace(tmp, CALL)
@@ -79,7 +84,12 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stderr}")
     os.replace(tmp, LIB)
-    _build_call()
+    if os.path.exists(CALL):  # one of an earlier build is not left beside this library
+        os.remove(CALL)
+    try:
+        _build_call()
+    except RuntimeError as e:
+        warnings.warn(f"the binding will call through ctypes: {e}", stacklevel=2)
     return LIB
 
 

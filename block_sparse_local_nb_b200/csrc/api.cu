@@ -251,7 +251,7 @@ const char* nb_status_string(int status) {
   }
 }
 
-int nb_abi_version(void) { return 100; }
+int nb_abi_version(void) { return NB_ABI_VERSION; }
 
 nb_status nb_kernel_error(int* code, int clear) {
   if (!code) return NB_ERR_INVALID_ARG;

@@ -40,7 +40,9 @@ bool convert(PyObject* o, T** out) {  // None, an address or a tensor
     *out = nullptr;
     return true;
   }
-  PyObject* at = PyLong_Check(o) ? Py_NewRef(o) : PyObject_CallMethodNoArgs(o, g_data_ptr);
+  PyObject* at = o;
+  if (PyLong_Check(o)) Py_INCREF(o);
+  else at = PyObject_CallMethodNoArgs(o, g_data_ptr);
   if (!at) return false;
   void* p = PyLong_AsVoidPtr(at);
   Py_DECREF(at);
@@ -92,5 +94,9 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_call", nullptr, -1, g_methods,
 
 PyMODINIT_FUNC PyInit__call() {
   g_data_ptr = PyUnicode_InternFromString("data_ptr");
-  return g_data_ptr ? PyModule_Create(&g_module) : nullptr;
+  if (!g_data_ptr) return nullptr;
+  PyObject* m = PyModule_Create(&g_module);
+  // the binding uses this module only beside a library of the same version
+  if (m && PyModule_AddIntConstant(m, "abi_version", NB_ABI_VERSION) < 0) Py_CLEAR(m);
+  return m;
 }

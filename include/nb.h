@@ -82,7 +82,8 @@ typedef enum nb_dtype {
 /* Human-readable name of a status code.  Never returns NULL. */
 NB_API const char* nb_status_string(int status);
 
-/* ABI version of this library (major * 100 + minor). */
+/* ABI version of this header, and of the library (major * 100 + minor). */
+#define NB_ABI_VERSION 101
 NB_API int nb_abi_version(void);
 
 /*
