@@ -69,8 +69,8 @@ def _strip_comments(src: str) -> str:
 # includes, and the files of operators that no workload here runs: changing them
 # cannot change a measured kernel's DRAM traffic.
 HOST_ONLY_SOURCES = ("attn_host.cu", "api.cu", "pycall.cpp")
-OTHER_OPERATORS = ("serving.cuh", "attn_sink_fwd.cu", "attn_sink_bwd.cu", "kv4.cuh", "kv4.cu",
-                   "attn_kv4_decode.cu")
+OTHER_OPERATORS = ("serving.cuh", "sink_hidden.cuh", "attn_sink_fwd.cu", "attn_sink_bwd.cu",
+                   "kv4.cuh", "kv4.cu", "attn_kv4_decode.cu")
 
 
 def kernel_source_hash() -> str:

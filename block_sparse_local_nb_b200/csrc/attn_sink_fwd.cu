@@ -22,6 +22,8 @@
 //              stage is free after its S product and a V stage only after P V.
 //              Rows past the sequence's length are set to zero in shared memory
 //              before the chunk is handed on: P is 0 there, but 0 x NaN is not.
+//              (Of the sinks' blocks the tensor map reads the sinks alone; what other
+//              hidden rows may do is mended at the end, sink_hidden.cuh.)
 //   warp 1     TMEM owner and S issuer (one thread): S_c = Q K_c^T (M 128, N 128)
 //              into three TMEM buffers at d = 64, two at d = 128.
 //   warp 2     P V issuer (one thread): O_h += P_c,h V_c,h (M 128, N d, K 64; P
@@ -38,8 +40,13 @@
 // and tears down (frees TMEM) instead of hanging.
 #include <math.h>
 
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
 #include "schedule.cuh"
 #include "serving.cuh"
+#include "sink_hidden.cuh"
 
 namespace nb {
 namespace {
@@ -82,6 +89,7 @@ struct Cfg {
   static constexpr int oSlot = oBar + nBar * 8;
   // per-tile hand-off of the halves' running max and sum to the epilogue warps:
   // [parity][half][m, l][row] fp32
+  static constexpr int oBad = oSlot + 8;  // some row of this CTA's tiles is not finite
   static constexpr int oXSum = oSlot + 16;
   static constexpr int oSched = oXSum + 2 * 2 * 2 * 128 * 4;  // work-order prefix table
   static constexpr int kSmem = oSched + kSchedBytes + 1024;  // + slack for 1024-byte alignment
@@ -254,10 +262,10 @@ __device__ int producer(const Params& p, const Sched& sch, uint32_t base, uint8_
 
 // V chunks (warp 3, the whole warp; lane 0 issues).  A chunk that reaches past
 // the sequence's length lands on a barrier of its own; the warp zeroes the rows
-// past the length and then hands the chunk on.
+// past the length and then hands the chunk on.  tf: V's map for the sinks' blocks.
 template <int D>
 __device__ int v_producer(const Params& p, uint32_t base, uint8_t* gbase, int lane,
-                          const CUtensorMap* tv) {
+                          const CUtensorMap* tv, const CUtensorMap* tf) {
   using C = Cfg<D>;
   const uint32_t bar = base + C::oBar;
   int fixes = 0;
@@ -283,8 +291,8 @@ __device__ int v_producer(const Params& p, uint32_t base, uint8_t* gbase, int la
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int s = 0; s < D / 64; ++s)
-              tma_load_3d(base + C::oV + st * C::kKBytes + s * kSlab + h * kHalf * 128, tv, land,
-                          s * 64, y[h], bkv);
+              tma_load_3d(base + C::oV + st * C::kKBytes + s * kSlab + h * kHalf * 128,
+                          2 * c + h < x.far ? tf : tv, land, s * 64, y[h], bkv);
         }
       }
       if (!__all_sync(0xffffffffu, ok)) return kErrVFree;
@@ -574,6 +582,7 @@ __device__ int epi_warps(const Params& p, uint32_t base, uint8_t* gbase, uint32_
   const bool leader = r == 0;
   auto all_ok = [](bool ok) { return __all_sync(0xffffffffu, ok); };
   int tc = 0;
+  uint32_t zeros[4] = {0u, 0u, 0u, 0u};  // no longer 0: some output was not finite
   for (int rd = 0;; ++rd) {
     Item x;
     if (!next_item<D>(x, rd, bar, gbase, lane)) return kErrIFull;
@@ -613,6 +622,8 @@ __device__ int epi_warps(const Params& p, uint32_t base, uint8_t* gbase, uint32_
                                           fmaf(o0[2 * i + 1], g0, o1[2 * i + 1] * g1))
                               : 0u;
       }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) zeros[i & 3] = hidden::add_zeros(w[i], zeros[i & 3]);
       if (s == D / 64 - 1) {  // the next tile's products may begin
         tc_fence_before();
         mbar_arrive(bar + 8 * C::bOFree);
@@ -633,14 +644,76 @@ __device__ int epi_warps(const Params& p, uint32_t base, uint8_t* gbase, uint32_
     ++tc;
   }
   if (leader) bulk_wait_all0();  // the last tile's store has landed before the CTA exits
+  if (hidden::word_bad(zeros[0]) || hidden::word_bad(zeros[1]) || hidden::word_bad(zeros[2]) ||
+      hidden::word_bad(zeros[3]))
+    *reinterpret_cast<volatile int*>(gbase + C::oBad) = 1;
   return 0;
+}
+
+// Rows of this CTA's tiles that are not finite and have a hidden row of V that is not
+// among their chunks' (sink_hidden.cuh), by the eight softmax warps, sixteen rows of a
+// tile each.
+template <int D>
+__device__ __forceinline__ void sum_again(const Params& p, const Sched& sch, int warp, int lane) {
+  using hidden::bf16;
+  const float sl2 = p.a.scale * kLog2e;
+  for (int rd = 0;; ++rd) {
+    const int it = item_at(rd);
+    if (it >= sch.count) break;
+    const Item x = sched_item(p, sch, it);
+    const int64_t bh = static_cast<int64_t>(x.b) * p.a.heads + x.h, bkv = bh / p.group;
+    const bf16* k = static_cast<const bf16*>(p.a.k) + bkv * p.a.n * D;
+    const bf16* v = static_cast<const bf16*>(p.a.v) + bkv * p.a.n * D;
+    const int brought = min(x.key(2 * x.nch - 1) + kHalf, x.L);  // end of the chunks' keys
+    for (int r = 0; r < kRows / 8 && x.nch > 0; ++r) {
+      const int q = x.tile * kRows + warp * (kRows / 8) + r;
+      if (q >= x.L) break;
+      bf16* out = static_cast<bf16*>(const_cast<void*>(p.a.o)) + (bh * p.a.n + q) * D;
+      const uint32_t bad = hidden::bad_channels<D>(out, lane);
+      if (!__any_sync(0xffffffffu, bad != 0)) continue;
+      const int first = q >= p.window ? q - p.window + 1 : 0, sinks = min(p.sinks, first);
+      if (!hidden::any_bad<D>(v, x.far ? x.k0 : max(x.k0, sinks), first, lane) &&
+          !hidden::any_bad<D>(v, q + 1, brought, lane))
+        continue;
+      const bf16* qrow = static_cast<const bf16*>(p.a.q) + (bh * p.a.n + q) * D;
+      hidden::Row<D> acc;
+      acc.zero();
+      float m = -INFINITY, l = 0.f;
+      bool more = true;
+      auto keys = [&](int from, int end) {
+        for (int base = from; base < end && more; base += 32) {
+          const int j = base + lane;
+          const float s = j < end ? sl2 * hidden::dot<D>(qrow, k + static_cast<int64_t>(j) * D)
+                                  : -INFINITY;
+          float mx = s;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          mx = fmaxf(mx, m);
+          const float sub = mx == -INFINITY ? 0.f : mx;
+          const float a = m == -INFINITY ? 0.f : ex2_approx(m - sub);
+          const float w = ex2_approx(s - sub);
+          m = mx;
+          l = l * a + w;
+          if (a != 1.f) acc.scale(a);
+          acc.add_rows(v, base, 0, min(32, end - base), w, lane);
+          more = !hidden::settled<D>(acc, bad);
+        }
+      };
+      keys(0, sinks);
+      keys(first, q + 1);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      acc.scale(1.f / l);
+      hidden::store_channels<D>(out, acc, bad, lane);
+    }
+  }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_sink_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
-                       const Params p) {
+                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tf,
+                       const __grid_constant__ CUtensorMap to, const Params p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -676,12 +749,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar + 8 * C::bVFix, 1);
     mbar_init(bar + 8 * C::bDone, 2);  // one commit per MMA-issuing thread
     fence_barrier_init();
+    *reinterpret_cast<volatile int*>(gbase + C::oBad) = 0;
   }
   if (warp == 0) {
     if (lane == 0) {
       prefetch_tmap(&tq);
       prefetch_tmap(&tk);
       prefetch_tmap(&tv);
+      prefetch_tmap(&tf);
       prefetch_tmap(&to);
     }
   }
@@ -703,13 +778,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0 && lane == 0) err = producer<D>(p, sch, base, gbase, &tq, &tk);
     if (warp == 1 && lane == 0) err = s_issuer<D>(base, gbase, tmem);
     if (warp == 2 && lane == 0) err = pv_issuer<D>(base, gbase, tmem);
-    if (warp == 3) err = v_producer<D>(p, base, gbase, lane, &tv);
+    if (warp == 3) err = v_producer<D>(p, base, gbase, lane, &tv, &tf);
   } else if (warp < 12) {
     regs_inc<C::kRegsSoft, kLaunchRegs>();
     err = softmax_warps<D>(p, sch, base, gbase, tmem, warp & 3, (warp - 4) >> 2, lane);
+    named_barrier(3, 384);  // the epilogue has stored every tile
+    if (*reinterpret_cast<volatile int*>(gbase + C::oBad)) sum_again<D>(p, sch, warp - 4, lane);
   } else {
     regs_dec<C::kRegsEpi, kLaunchRegs>();
     err = epi_warps<D>(p, base, gbase, tmem, warp & 3, lane, &to);
+    named_barrier(3, 384);
   }
   if (err) record_error(p.a.err, err);
 
@@ -727,19 +805,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
 template <int D>
 cudaError_t launch(const SinkArgs& g, cudaStream_t stream) {
   using C = Cfg<D>;
   const int64_t heads_total = static_cast<int64_t>(g.batch) * g.heads;
   const int64_t kv_total = static_cast<int64_t>(g.batch) * g.kv_heads;
-  CUtensorMap tq, tk, tv, to;
+  CUtensorMap tq, tk, tv, tf, to;
   if (!make_tmap_bf16_rows(&tq, g.q, D, g.n, heads_total, kRows) ||
       !make_tmap_bf16_rows(&tk, g.k, D, g.n, kv_total, kHalf) ||
       !make_tmap_bf16_rows(&tv, g.v, D, g.n, kv_total, kHalf) ||
       !make_tmap_bf16_rows(&to, g.o, D, g.n, heads_total, kRows))
     return cudaErrorInvalidValue;
+  tf = tv;  // without sinks, or with every key in every window, no tile has blocks of sinks
+  if (g.sinks > 0 && g.n > g.window &&
+      !make_tmap_first_rows(&tf, g.v, D, g.n, kv_total, g.sinks, kHalf))
+    return cudaErrorInvalidValue;
   Params p;
   p.a = AttnArgs{};
+  p.a.q = g.q;
+  p.a.k = g.k;
+  p.a.v = g.v;
   p.a.o = g.o;
   p.a.lse = g.lse;
   p.a.lengths = g.lengths;
@@ -761,10 +849,32 @@ cudaError_t launch(const SinkArgs& g, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int grid = static_cast<int>(items < num_sms() ? items : num_sms());
   return launch_pdl(attn_sink_fwd_kernel<D>, dim3(grid), dim3(kThreads), C::kSmem, stream, tq, tk,
-                    tv, to, p);
+                    tv, tf, to, p);
 }
 
 }  // namespace
+
+bool make_tmap_first_rows(CUtensorMap* m, const void* base, int d, int64_t n, int64_t heads_total,
+                          int first, int box_rows) {
+  std::call_once(g_encode_once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  if (!g_encode) return false;
+  const int64_t rows = first < 1 ? 1 : (first < n ? first : n);
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(heads_total)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(n) * d * 2};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_rows), 1u}, steps[3] = {1u, 1u, 1u};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                  box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 cudaError_t launch_attn_sink_fwd(const SinkArgs& a, cudaStream_t stream) {
   return a.d == 64 ? launch<64>(a, stream) : launch<128>(a, stream);

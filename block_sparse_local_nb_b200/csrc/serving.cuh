@@ -82,6 +82,9 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// make_tmap_bf16_rows whose loads read 0 from row `first` (at least 1) of every head on.
+bool make_tmap_first_rows(CUtensorMap* m, const void* base, int d, int64_t n, int64_t heads_total,
+                          int first, int box_rows);
 cudaError_t launch_attn_sink_fwd(const SinkArgs& a, cudaStream_t stream);
 size_t sink_bwd_workspace_bytes(const SinkArgs& a);
 cudaError_t launch_attn_sink_bwd(const SinkArgs& a, cudaStream_t stream);

@@ -313,6 +313,8 @@ NB_API nb_status nb_batch_ceiling(const int64_t* offsets, int batch, int k, int3
  * o, lse  out: as nb_attn_fwd (lse may be NULL).
  * lengths in : int32 [batch] or NULL (see conventions).  What rows past a
  *              sequence's length hold, NaN included, does not matter.
+ * A NaN or an infinity in K or V reaches the queries that see its token, and no other.
+ * (Queries whose tile it shares are summed again, which takes time but only then.)
  * n >= 0, any value; window >= 1 (n or more: plain causal attention);
  * 0 <= sinks <= NB_MAX_SINKS (more returns NB_ERR_UNSUPPORTED).
  * NB_BF16 only (NB_F32 returns NB_ERR_UNSUPPORTED).
