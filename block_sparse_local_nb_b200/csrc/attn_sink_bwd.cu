@@ -33,7 +33,8 @@
 // Warp roles (512 threads, four warpgroups with reallocated registers): warp 0
 // takes the items, decodes them for the others into a ring in shared memory, and
 // is the TMA producer (a chunk that reaches past the length lands on a barrier of its
-// own, and the warp zeroes the rows past it: P is 0 there, but 0 x NaN is not);
+// own, and the warp zeroes the rows past it: P is 0 there, but 0 x NaN is not; what other
+// hidden rows may do is mended at the end, sink_hidden.cuh);
 // warp 1 TMEM owner and S/dP issuer; warp 2 issuer of the gradient products;
 // warpgroups 1 and 2 take the chunks in turn (thread = lane, 64 columns): a group
 // moves S and dP into registers and hands their columns back at once, so the next
@@ -44,6 +45,7 @@
 #include <math.h>
 
 #include "serving.cuh"
+#include "sink_hidden.cuh"
 
 namespace nb {
 namespace {
@@ -80,6 +82,7 @@ struct Params {
   int items;     // of the main kernel
   int term_blocks;  // of the row kernel: those of rows that see few keys
   int* taken;    // items taken so far by the CTAs of <kDQ = false>, <kDQ = true>
+  int* noted;    // [items][4]: quarter tiles with rows that are not finite, linked (epi_warps)
   float scale;
 };
 
@@ -143,7 +146,9 @@ struct Cfg {
                        bIFree = bIFull + kItems, bFix = bIFree + kItems, bDone = bFix + 2,
                        nBar = bDone + 1;
   static constexpr int oSlot = oBar + nBar * 8;
-  static constexpr int oPre = oSlot + 16;  // work table: pre[0..batch], len[0..batch)
+  static constexpr int oNoted = oSlot + 16;  // of each epilogue warp: its last noted quarter, or -1
+  static constexpr int oFound = oNoted + 16;  // of every fourth tile: some value is not finite
+  static constexpr int oPre = oFound + 16;  // work table: pre[0..batch], len[0..batch)
   static constexpr int kSmem = oPre + (2 * kMaxBatch + 1) * 4 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
   static constexpr uint32_t kTmemCols = 512;
@@ -167,6 +172,7 @@ struct Item {
   int nq;             // chunks per head (key tiles)
   int k0, far;        // kDQ: first key of the window's chunks, chunks of sinks before them
   int part, parts;    // key tiles: this item's part
+  int id;             // its place in the list
 };
 
 // Items of a sequence of length L (kDQ: query tiles of all heads; else the key
@@ -217,6 +223,7 @@ template <int D, bool kDQ>
 __device__ Item item(const Params& p, const int* pre, int k) {
   constexpr int kChunk = chunk_rows(D, kDQ);
   Item x;
+  x.id = k;
   x.c0 = x.nch = x.nq = x.k0 = x.far = x.part = 0;
   x.parts = 1;
   const int lead = first_items<kDQ>(p);
@@ -357,10 +364,11 @@ __device__ __forceinline__ int load_chunk(const Params& p, int L, Chunk k, uint3
 }
 
 // Items, tiles and the chunks' operands, kSplit: X alone (warp 0, the whole warp).
+// cf: X's map for the chunks of sinks (kDQ).
 template <int D, bool kDQ>
 __device__ int producer(const Params& p, const int* pre, uint32_t base, uint8_t* gbase, int lane,
                         const CUtensorMap* tx, const CUtensorMap* ty, const CUtensorMap* cx,
-                        const CUtensorMap* cy) {
+                        const CUtensorMap* cf, const CUtensorMap* cy) {
   using C = Cfg<D, kDQ>;
   const uint32_t bar = base + C::oBar;
   const int count = item_count<kDQ>(p, pre);
@@ -416,8 +424,9 @@ __device__ int producer(const Params& p, const int* pre, uint32_t base, uint8_t*
                       lane != 0 || mbar_wait(bar + 8 * (C::bXFree + ring.i), ring.ph ^ 1)))
         return kErrXFree;
       const int err = load_chunk<D, kDQ, !C::kSplit>(
-          p, x.L, chunk<D, kDQ>(p, x, c), base, gbase, cx, C::oX + ring.i * C::kHalf, cy,
-          C::oY + ring.i * C::kHalf, bar + 8 * (C::bXFull + ring.i), bar + 8 * C::bFix, fixes,
+          p, x.L, chunk<D, kDQ>(p, x, c), base, gbase, kDQ && c < x.far ? cf : cx,
+          C::oX + ring.i * C::kHalf, cy, C::oY + ring.i * C::kHalf,
+          bar + 8 * (C::bXFull + ring.i), bar + 8 * C::bFix, fixes,
           kDQ ? 0 : base + C::oCol + ring.i * 2 * C::kChunk * 4, lane);
       if (err) return err;
       ring.next();
@@ -764,6 +773,16 @@ __device__ int grad_warps(const Params& p, uint32_t base, uint8_t* gbase,
   return 0;
 }
 
+// Where the part of a split key tile goes ([dV, dK][128][D]), or null.
+template <int D>
+__device__ __forceinline__ float* part_of(const Params& p, const Item& x, int bh) {
+  if (x.parts <= 1) return nullptr;
+  const int64_t slot =
+      x.tile == 0 ? static_cast<int64_t>(bh) * p.s0 + x.part
+                  : (static_cast<int64_t>(bh) * (p.ntiles - 1) + x.tile - 1) * p.s1 + x.part;
+  return (x.tile == 0 ? p.part0 : p.part1) + slot * 2 * kRows * D;
+}
+
 // Gradients of finished items (warpgroup 3, thread = lane r): bf16 tiles through
 // the staging buffer and a TMA store, or fp32 parts straight to the workspace.
 template <int D, bool kDQ>
@@ -776,23 +795,22 @@ __device__ int epi_warps(const Params& p, uint32_t base, uint8_t* gbase,
   const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16);
   const bool leader = r == 0;
   auto all_ok = [](bool ok) { return __all_sync(0xffffffffu, ok); };
-  int tc = 0;
+  int tc = 0, noted = -1;
+  volatile int* found = reinterpret_cast<volatile int*>(gbase + C::oFound);
   for (int rd = 0;; ++rd) {
     Item x;
     if (!next_item<D, kDQ>(x, rd, bar, gbase, lane)) return kErrIFull;
     if (x.nch < 0) break;
+    // a hidden row that is not finite makes a column of the whole tile so, in rows past the
+    // length too: each warp looks at a quarter of the columns, for all four
+    float2 zeros[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     const int acc = tc % C::NACC;
     if (!all_ok(mbar_wait(bar + 8 * (C::bAFull + acc), (tc / C::NACC) & 1))) return kErrAFull;
     tc_fence_after();
     const bool valid = x.tile * kRows + r < x.L;
     const int bh = x.b * (kDQ ? p.heads : p.kv_heads) + x.h;
-    float* part = nullptr;
-    if (!kDQ && x.parts > 1) {
-      const int64_t slot =
-          x.tile == 0 ? static_cast<int64_t>(bh) * p.s0 + x.part
-                      : (static_cast<int64_t>(bh) * (p.ntiles - 1) + x.tile - 1) * p.s1 + x.part;
-      part = (x.tile == 0 ? p.part0 : p.part1) + slot * 2 * kRows * D + r * D;
-    }
+    float* part = kDQ ? nullptr : part_of<D>(p, x, bh);
+    if (part != nullptr) part += r * D;
 #pragma unroll
     for (int out = 0; out < C::NOUT; ++out) {
       const float mul = kDQ || out == 1 ? p.scale : 1.f;  // dQ, dK; dV
@@ -809,31 +827,47 @@ __device__ int epi_warps(const Params& p, uint32_t base, uint8_t* gbase,
           tmem_ld32(trow + C::tAcc(acc, out) + col, v);
           tmem_wait_ld();
           reg_fence(v);
+          float2 x[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = valid ? v[i] * mul : 0.f;
+          for (int i = 0; i < 16; ++i)
+            x[i] = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(mul, mul));
+#pragma unroll
+          for (int e = 0; e < 2; ++e)  // 16 columns of 64
+            if (wq == 2 * j + e) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                zeros[i & 1] = __ffma2_rn(x[8 * e + i], make_float2(0.f, 0.f), zeros[i & 1]);
+            }
           if (part != nullptr) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               *reinterpret_cast<float4*>(part + out * kRows * D + col + 4 * i) =
-                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                  valid ? make_float4(x[2 * i].x, x[2 * i].y, x[2 * i + 1].x, x[2 * i + 1].y)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
           } else {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = valid ? pack_bf16(x[i].x, x[i].y) : 0u;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const int gc = 4 * j + u;  // 16-byte chunk of the slab's row
               *reinterpret_cast<uint4*>(gbase + C::oStg + r * 128 + ((gc ^ (r & 7)) << 4)) =
-                  make_uint4(pack_bf16(v[8 * u], v[8 * u + 1]), pack_bf16(v[8 * u + 2], v[8 * u + 3]),
-                             pack_bf16(v[8 * u + 4], v[8 * u + 5]),
-                             pack_bf16(v[8 * u + 6], v[8 * u + 7]));
+                  make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
             }
           }
         }
-        if (out == C::NOUT - 1 && sl == D / 64 - 1) {
+        const bool last = out == C::NOUT - 1 && sl == D / 64 - 1;
+        if (last) {
           tc_fence_before();
           mbar_arrive(bar + 8 * (C::bAFree + acc));
+          const float z = (zeros[0].x + zeros[0].y) + (zeros[1].x + zeros[1].y);
+          if (z != z) found[tc & 3] = 1;
+          // read by all before the last tile's barrier, set by none before this one's
+          if (leader) found[(tc + 2) & 3] = 0;
         }
+        if (part == nullptr) fence_proxy_async_smem();
+        if (part == nullptr || last) named_barrier(1, 128);
         if (part == nullptr) {
-          fence_proxy_async_smem();
-          named_barrier(1, 128);
           if (leader) {
             tma_store_3d(out == 0 ? to0 : to1, base + C::oStg, sl * 64, x.tile * kRows, bh);
             bulk_commit();
@@ -841,19 +875,148 @@ __device__ int epi_warps(const Params& p, uint32_t base, uint8_t* gbase,
         }
       }
     }
+    if (found[tc & 3]) {
+      if (lane == 0) p.noted[4 * x.id + wq] = noted;
+      noted = 4 * x.id + wq;
+    }
     ++tc;
   }
   if (leader) bulk_wait_all0();
+  if (lane == 0) *reinterpret_cast<volatile int*>(gbase + C::oNoted + 4 * wq) = noted;
   return 0;
 }
 
-// tx, ty: the tile that stays (K, V or Q, dO); cx, cy: the chunks (Q, dO or K, V);
-// to0, to1: dV, dK or dQ twice.
+// The rows of dQ that the epilogue noted and that have a hidden row of K that is not
+// finite among their chunks' (sink_hidden.cuh): eight warps, two to a quarter tile.
+template <int D>
+__device__ __forceinline__ void sum_queries_again(const Params& p, const int* pre, int at, int second,
+                                                  int lane) {
+  using hidden::bf16;
+  const float sl2 = p.scale * kLog2e;
+  for (; at >= 0; at = __ldcg(p.noted + at)) {
+    const Item x = item<D, true>(p, pre, at >> 2);
+    const int64_t bh = static_cast<int64_t>(x.b) * p.heads + x.h;
+    const int64_t bkv = static_cast<int64_t>(x.b) * p.kv_heads + x.h / p.group;
+    const bf16* k = static_cast<const bf16*>(p.k) + bkv * p.n * D;
+    const bf16* v = static_cast<const bf16*>(p.v) + bkv * p.n * D;
+    // end of the chunks' keys
+    const int brought = min(x.k0 + (x.nch - x.far) * chunk_rows(D, true), x.L);
+    for (int r = 0; r < 16; ++r) {
+      const int q = x.tile * kRows + 32 * (at & 3) + 16 * second + r;
+      if (q >= x.L) break;
+      bf16* out = static_cast<bf16*>(p.dq) + (bh * p.n + q) * D;
+      const uint32_t bad = hidden::bad_channels<D>(out, lane);
+      if (!__any_sync(0xffffffffu, bad != 0)) continue;
+      const int first = q >= p.window ? q - p.window + 1 : 0, sinks = min(p.sinks, first);
+      if (!hidden::any_bad<D>(k, x.far ? x.k0 : max(x.k0, sinks), first, lane) &&
+          !hidden::any_bad<D>(k, q + 1, brought, lane))
+        continue;
+      const bf16* qrow = static_cast<const bf16*>(p.q) + (bh * p.n + q) * D;
+      const bf16* grow = static_cast<const bf16*>(p.dout) + (bh * p.n + q) * D;
+      const float nl = p.nlse2[bh * p.npad + q], nd = p.nd[bh * p.npad + q];
+      hidden::Row<D> acc;
+      acc.zero();
+      bool more = true;
+      auto keys = [&](int from, int end) {
+        for (int base = from; base < end && more; base += 32) {
+          const int64_t j = min(base + lane, end - 1);
+          const float s = hidden::dot<D>(qrow, k + j * D), dp = hidden::dot<D>(grow, v + j * D);
+          acc.add_rows(k, base, 0, min(32, end - base), ex2_approx(fmaf(s, sl2, nl)) * (dp + nd), lane);
+          more = !hidden::settled<D>(acc, bad);
+        }
+      };
+      keys(0, sinks);
+      keys(first, q + 1);
+      acc.scale(p.scale);
+      hidden::store_channels<D>(out, acc, bad, lane);
+    }
+  }
+}
+
+// The same of dV (hidden rows of dO) and dK (of Q), in bf16 or in the item's part.
+template <int D>
+__device__ __forceinline__ void sum_keys_again(const Params& p, const int* pre, int at, int second,
+                                               int lane) {
+  using hidden::bf16;
+  constexpr int kChunk = chunk_rows(D, false);
+  const float sl2 = p.scale * kLog2e;
+  for (; at >= 0; at = __ldcg(p.noted + at)) {
+    const Item x = item<D, false>(p, pre, at >> 2);
+    const int bh = x.b * p.kv_heads + x.h;
+    float* part = part_of<D>(p, x, bh);
+    for (int r = 0; r < 16; ++r) {
+      const int row = 32 * (at & 3) + 16 * second + r, key = x.tile * kRows + row;
+      if (key >= x.L) break;
+      const int64_t place = (static_cast<int64_t>(bh) * p.n + key) * D;
+      bf16* dv = static_cast<bf16*>(p.dv) + place;
+      bf16* dk = static_cast<bf16*>(p.dk) + place;
+      float* pv = part + row * D;  // unused without a part
+      float* pk = pv + kRows * D;
+      const uint32_t badv = part ? hidden::bad_channels<D>(pv, lane) : hidden::bad_channels<D>(dv, lane);
+      const uint32_t badk = part ? hidden::bad_channels<D>(pk, lane) : hidden::bad_channels<D>(dk, lane);
+      if (!__any_sync(0xffffffffu, (badv | badk) != 0)) continue;
+      const int end = key < p.sinks ? x.L  // of the queries that see the key
+                                    : static_cast<int>(min(static_cast<int64_t>(key) + p.window,
+                                                           static_cast<int64_t>(x.L)));
+      const bf16* krow = static_cast<const bf16*>(p.k) + place;
+      const bf16* vrow = static_cast<const bf16*>(p.v) + place;
+      // every chunk's queries of the item: visible ones are [lo, hi)
+      auto chunks = [&](auto&& f) {
+        for (int c = 0; c < x.nch; ++c) {
+          const Chunk ch = chunk<D, false>(p, x, c);
+          const int lo = max(ch.row, key), hi = min(ch.row + kChunk, end);
+          if (!f(ch, lo, hi)) return false;
+        }
+        return true;
+      };
+      // (beside the sinks nearly all queries are hidden, and few are seen: these rows are
+      // summed without the look)
+      if (!(x.tile == 0 && p.sinks > 0 && key >= p.sinks) &&
+          chunks([&](const Chunk& ch, int lo, int hi) {
+            const bf16* q = static_cast<const bf16*>(p.q) + static_cast<int64_t>(ch.bh) * p.n * D;
+            const bf16* g = static_cast<const bf16*>(p.dout) + static_cast<int64_t>(ch.bh) * p.n * D;
+            const int last = min(ch.row + kChunk, x.L), a = min(lo, last), b = max(hi, ch.row);
+            return !(hidden::any_bad<D>(q, ch.row, a, lane) || hidden::any_bad<D>(g, ch.row, a, lane) ||
+                     hidden::any_bad<D>(q, max(a, b), last, lane) ||
+                     hidden::any_bad<D>(g, max(a, b), last, lane));
+          }))
+        continue;
+      hidden::Row<D> av, ak;
+      av.zero();
+      ak.zero();
+      chunks([&](const Chunk& ch, int lo, int hi) {
+        const bf16* q = static_cast<const bf16*>(p.q) + static_cast<int64_t>(ch.bh) * p.n * D;
+        const bf16* g = static_cast<const bf16*>(p.dout) + static_cast<int64_t>(ch.bh) * p.n * D;
+        const int64_t stats = static_cast<int64_t>(ch.bh) * p.npad;
+        for (int from = lo; from < hi; from += 32) {
+          const int j = min(from + lane, hi - 1);
+          const float s = hidden::dot<D>(krow, q + static_cast<int64_t>(j) * D);
+          const float dp = hidden::dot<D>(vrow, g + static_cast<int64_t>(j) * D);
+          const float w = ex2_approx(fmaf(s, sl2, p.nlse2[stats + j]));
+          av.add_rows(g, from, 0, min(32, hi - from), w, lane);
+          ak.add_rows(q, from, 0, min(32, hi - from), w * (dp + p.nd[stats + j]), lane);
+        }
+        return !(hidden::settled<D>(av, badv) && hidden::settled<D>(ak, badk));
+      });
+      ak.scale(p.scale);
+      if (part) {
+        hidden::store_channels<D>(pv, av, badv, lane);
+        hidden::store_channels<D>(pk, ak, badk, lane);
+      } else {
+        hidden::store_channels<D>(dv, av, badv, lane);
+        hidden::store_channels<D>(dk, ak, badk, lane);
+      }
+    }
+  }
+}
+
+// tx, ty: the tile that stays (K, V or Q, dO); cx, cy: the chunks (Q, dO or K, V); cf: the
+// chunks of sinks (K); to0, to1: dV, dK or dQ twice.
 template <int D, bool kDQ>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_sink_bwd_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty,
-                         const __grid_constant__ CUtensorMap cx, const __grid_constant__ CUtensorMap cy,
-                         const __grid_constant__ CUtensorMap to0,
+                         const __grid_constant__ CUtensorMap cx, const __grid_constant__ CUtensorMap cf,
+                         const __grid_constant__ CUtensorMap cy, const __grid_constant__ CUtensorMap to0,
                          const __grid_constant__ CUtensorMap to1, const Params p) {
   using C = Cfg<D, kDQ>;
   extern __shared__ uint8_t smem_raw[];
@@ -896,11 +1059,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(bar + 8 * C::bDone, 2);  // one commit per MMA-issuing thread
     fence_barrier_init();
+    for (int i = 0; i < 4; ++i) {
+      *reinterpret_cast<volatile int*>(gbase + C::oNoted + 4 * i) = -1;
+      *reinterpret_cast<volatile int*>(gbase + C::oFound + 4 * i) = 0;
+    }
   }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tx);
     prefetch_tmap(&ty);
     prefetch_tmap(&cx);
+    if (kDQ) prefetch_tmap(&cf);
     prefetch_tmap(&cy);
     prefetch_tmap(&to0);
     prefetch_tmap(&to1);
@@ -924,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int err = 0;
   if (warp < 4) {
     regs_dec<C::kRegsCtl, kLaunchRegs>();
-    if (warp == 0) err = producer<D, kDQ>(p, pre, base, gbase, lane, &tx, &ty, &cx, &cy);
+    if (warp == 0) err = producer<D, kDQ>(p, pre, base, gbase, lane, &tx, &ty, &cx, &cf, &cy);
     if (warp == 1 && lane == 0) err = s_issuer<D, kDQ>(p, base, gbase, tmem);
     if (warp == 2 && lane == 0) err = grad_issuer<D, kDQ>(p, base, gbase, tmem);
     if (C::kSplit && warp == 3) err = y_producer<D, kDQ>(p, base, gbase, lane, &cy);
@@ -948,6 +1116,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
+  }
+  // The epilogue has stored every tile.  (Last, so that the code above stays together: in
+  // the warps' own branch this cost 0.6 us a launch without being run.)
+  if (warp >= 4 && warp < 12) {
+    const int noted = *reinterpret_cast<volatile int*>(gbase + C::oNoted + 4 * (warp & 3));
+    if (kDQ) sum_queries_again<D>(p, pre, noted, (warp - 4) >> 2, lane);
+    else sum_keys_again<D>(p, pre, noted, (warp - 4) >> 2, lane);
   }
 }
 
@@ -1145,7 +1320,7 @@ __global__ void __launch_bounds__(256) sink_join_kernel(const Params p, int tile
 
 struct Plan {
   int npad, ntiles, s0, s1;
-  int64_t taken, nd, nlse2, part0, part1, bytes;  // workspace offsets and size
+  int64_t taken, nd, nlse2, noted, part0, part1, bytes;  // workspace offsets and size
 };
 
 // Cuts key tiles into parts: the first ones when they are more than a third of an
@@ -1182,7 +1357,11 @@ Plan make_plan(const SinkArgs& a) {
   w.taken = 0;
   w.nd = 256;
   w.nlse2 = w.nd + align_up(rows * 4, 256);
-  w.part0 = w.nlse2 + align_up(rows * 4, 256);
+  w.noted = w.nlse2 + align_up(rows * 4, 256);
+  // four words an item, of the kernel that has more of them
+  const int64_t tiles_q = static_cast<int64_t>(a.batch) * a.heads * w.ntiles;
+  const int64_t tiles_k = bkv * (w.s0 + static_cast<int64_t>(w.ntiles - 1) * w.s1);
+  w.part0 = w.noted + align_up((tiles_q > tiles_k ? tiles_q : tiles_k) * 16, 256);
   w.part1 = w.part0 + (w.s0 > 1 ? bkv * w.s0 * tile : 0);
   w.bytes = w.part1 + (w.s1 > 1 ? bkv * (w.ntiles - 1) * w.s1 * tile : 0);
   return w;
@@ -1193,7 +1372,7 @@ cudaError_t launch_main(const SinkArgs& a, Params p, cudaStream_t stream) {
   using C = Cfg<D, kDQ>;
   const int64_t hq = static_cast<int64_t>(a.batch) * a.heads;
   const int64_t hk = static_cast<int64_t>(a.batch) * a.kv_heads;
-  CUtensorMap tx, ty, cx, cy, to0, to1;
+  CUtensorMap tx, ty, cx, cf, cy, to0, to1;
   const bool maps =
       kDQ ? make_tmap_bf16_rows(&tx, a.q, D, a.n, hq, kRows) &&
                 make_tmap_bf16_rows(&ty, a.dout, D, a.n, hq, kRows) &&
@@ -1208,16 +1387,20 @@ cudaError_t launch_main(const SinkArgs& a, Params p, cudaStream_t stream) {
                 make_tmap_bf16_rows(&to0, a.dv, D, a.n, hk, kRows) &&
                 make_tmap_bf16_rows(&to1, a.dk, D, a.n, hk, kRows);
   if (!maps) return cudaErrorInvalidValue;
+  cf = cx;  // without sinks, or with every key in every window, no tile has chunks of sinks
+  if (kDQ && a.sinks > 0 && a.n > a.window &&
+      !make_tmap_first_rows(&cf, a.k, D, a.n, hk, a.sinks, C::kChunk))
+    return cudaErrorInvalidValue;
   const int64_t items = kDQ ? hq * p.ntiles
                             : hk * (p.s0 + static_cast<int64_t>(p.ntiles - 1) * p.s1);
-  if (items > (1ll << 30)) return cudaErrorInvalidValue;
+  if (items > (1ll << 28)) return cudaErrorInvalidValue;  // four words each are numbered in 31 bits
   p.items = static_cast<int>(items);
   cudaError_t e = cudaFuncSetAttribute(attn_sink_bwd_kernel<D, kDQ>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const int grid = static_cast<int>(items < num_sms() ? items : num_sms());
   return launch_pdl(attn_sink_bwd_kernel<D, kDQ>, dim3(grid), dim3(kThreads), C::kSmem, stream, tx,
-                    ty, cx, cy, to0, to1, p);
+                    ty, cx, cf, cy, to0, to1, p);
 }
 
 template <int D>
@@ -1238,6 +1421,7 @@ cudaError_t run(const SinkArgs& a, cudaStream_t stream) {
   p.taken = reinterpret_cast<int*>(ws + w.taken);
   p.nd = reinterpret_cast<float*>(ws + w.nd);
   p.nlse2 = reinterpret_cast<float*>(ws + w.nlse2);
+  p.noted = reinterpret_cast<int*>(ws + w.noted);
   p.part0 = reinterpret_cast<float*>(ws + w.part0);
   p.part1 = reinterpret_cast<float*>(ws + w.part1);
   p.err = a.err;

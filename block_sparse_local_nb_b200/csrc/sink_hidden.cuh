@@ -3,11 +3,14 @@
 // The tensor cores multiply every row of a tile with every row of a chunk, and the mask
 // enters as a weight of 0.  Where the hidden row of the chunk holds a NaN or an infinity,
 // 0 times it is NaN.  Finite inputs never meet this, so nothing of it stands in the path of
-// a chunk: the epilogue notes rows that came out non-finite (32 packed multiply-adds for 64
-// columns), and when a block has finished its tiles, its warps look at such rows
-// again: a row that only visible values made non-finite stays, and one with a non-finite
-// hidden row among its chunks' is summed once more over the rows that it sees, in fp32 and
-// in a fixed order.  That takes some 20 cycles a key and row; the other rows keep their bits.
+// a chunk: the epilogue notes rows that came out non-finite (a multiply-add for two
+// values), and when a block has finished its tiles, its warps look at such rows again: a
+// row that only visible values made non-finite stays, and one with a non-finite hidden row
+// among its chunks' is summed once more over the rows that it sees, in fp32 and in a fixed
+// order; the other rows keep their bits.  (Each lane reads a row of its own 16 bytes at a
+// time, which binds it: one bad token makes a forward of 32768 x 64 with window 1024 1.2 ms
+// longer, of 32768 x 128 2.2 ms.  Clean inputs pay 0.3 to 0.8 % for the notes,
+// forward and backward of 2 x 4 heads x 333 x 64 1.4 %, 0.5 us.)
 // The sinks' blocks, which every later tile reads, would make this the common case for one
 // bad token near a sequence's begin: there the tensor map itself ends with the sinks.
 #pragma once
@@ -52,7 +55,7 @@ __device__ __forceinline__ float dot(const bf16* a, const bf16* b) {
   const uint4* pa = reinterpret_cast<const uint4*>(a);
   const uint4* pb = reinterpret_cast<const uint4*>(b);
   float s = 0.f;
-#pragma unroll 8
+#pragma unroll 4
   for (int i = 0; i < D / 8; ++i) {
     const uint4 x = pa[i], y = pb[i];
     const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
@@ -91,7 +94,7 @@ struct Row {
   // sum_j weight_j row_j over the rows base + jj, lo <= jj < hi; lane jj holds weight_jj
   __device__ __forceinline__ void add_rows(const bf16* x, int64_t base, int lo, int hi, float weight,
                                            int lane) {
-#pragma unroll 16
+#pragma unroll 8
     for (int jj = lo; jj < hi; ++jj)
       add(x + (base + jj) * D, __shfl_sync(0xffffffffu, weight, jj), lane);
   }
@@ -111,12 +114,29 @@ __device__ __forceinline__ uint32_t bad_channels(const bf16* row, int lane) {
   }
   return bad;
 }
+// The same of a row of fp32 written by other threads of this block.
+template <int D>
+__device__ __forceinline__ uint32_t bad_channels(const float* row, int lane) {
+  uint32_t bad = 0;
+#pragma unroll
+  for (int i = 0; i < Row<D>::N; ++i) {
+    const uint32_t w = __float_as_uint(__ldcg(row + Row<D>::N * lane + i));
+    if ((w & 0x7f800000u) == 0x7f800000u) bad |= 1u << i;
+  }
+  return bad;
+}
 // Writes the channels of `which`.
 template <int D>
 __device__ __forceinline__ void store_channels(bf16* row, const Row<D>& r, uint32_t which, int lane) {
 #pragma unroll
   for (int i = 0; i < Row<D>::N; ++i)
     if (which >> i & 1u) row[Row<D>::N * lane + i] = __float2bfloat16_rn(r.v[i]);
+}
+template <int D>
+__device__ __forceinline__ void store_channels(float* row, const Row<D>& r, uint32_t which, int lane) {
+#pragma unroll
+  for (int i = 0; i < Row<D>::N; ++i)
+    if (which >> i & 1u) row[Row<D>::N * lane + i] = r.v[i];
 }
 // Every channel of `which`, in all lanes, is NaN: no further term changes the row.
 template <int D>

@@ -335,6 +335,8 @@ NB_API nb_status nb_attn_sink_fwd(const void* q, const void* k, const void* v, v
  * dq         out: [batch, heads, n, d];  dk, dv out: [batch, kv_heads, n, d].
  *                 Rows past a sequence's length are written as 0.  The outputs
  *                 must not alias the inputs.
+ * A NaN or an infinity in Q, K, V, O or dO reaches the gradients that depend on it by
+ * these formulas over the visible pairs, and no other.
  * workspace     : device scratch of at least nb_attn_sink_bwd_workspace_size(...)
  *                 bytes, 256-byte aligned; contents on entry do not matter.  It
  *                 must not be used by another call that runs concurrently.
