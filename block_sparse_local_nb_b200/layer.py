@@ -120,6 +120,13 @@ def block_sparse_local_attention(q, k, v, lengths=None, R: int = 1, causal: bool
     return BlockSparseLocalAttention.apply(q, k, v, lengths, R, causal)
 
 
+def _dense(x):
+    """x contiguous and 16-byte aligned, as the library takes it (a gradient or a cache row
+    may be a contiguous view at an odd offset): itself, or a copy."""
+    x = x.contiguous()
+    return x if x.data_ptr() % 16 == 0 else x.clone()
+
+
 def _c_int(x) -> int:
     """A Python integer as the library's 32-bit one: the nearest (a window or sinks
     beyond it mean the same, or are refused all the same)."""
@@ -148,7 +155,7 @@ class SinkAttention(torch.autograd.Function):
         if not (q.device == k.device == v.device):
             raise ValueError("q, k, v must be on one device")
         window, sinks = _c_int(window), _c_int(sinks)
-        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        q, k, v = _dense(q), _dense(k), _dense(v)
         if lengths is not None:
             if lengths.shape != (batch,):
                 raise ValueError("lengths must be [batch]")
@@ -167,7 +174,7 @@ class SinkAttention(torch.autograd.Function):
     def backward(ctx, do):
         q, k, v, o, lse, lengths = ctx.saved_tensors
         batch, heads, n, d = q.shape
-        do = do.to(q.dtype).contiguous()
+        do = _dense(do.to(q.dtype))
         shape = (batch, heads, k.shape[1], n, d, ctx.window, ctx.sinks, _dtype_code(q))
         ws_bytes = nb.attn_sink_bwd_workspace_size(*shape)
         ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=q.device)
@@ -214,7 +221,7 @@ class KV4Cache:
             raise ValueError(f"{name} must be [{self.batch}, {self.kv_heads}, n, {self.d}]")
         if x.device != self.device:
             raise ValueError(f"{name} must be on the cache's device, {self.device}")
-        return x.contiguous()
+        return _dense(x)
 
     def _per_sequence(self, x, name):
         if x.shape != (self.batch,):
@@ -263,7 +270,7 @@ class KV4Cache:
         if q.device != self.device:
             raise ValueError(f"q must be on the cache's device, {self.device}")
         window, sinks = _c_int(window), _c_int(sinks)
-        q = q.contiguous()
+        q = _dense(q)
         heads, code = q.shape[1], _dtype_code(q)
         o = torch.empty_like(q)
         size = nb.attn_kv4_decode_workspace_size(self.batch, heads, self.kv_heads, self.d,
