@@ -154,9 +154,10 @@ nb_status check_sink(int batch, int heads, int kv_heads, int n, int d, int windo
   if (dtype != NB_F32 && dtype != NB_BF16) return NB_ERR_INVALID_ARG;
   if ((d != 64 && d != 128) || dtype != NB_BF16 || sinks > NB_MAX_SINKS) return NB_ERR_UNSUPPORTED;
   if (heads > 65535 || batch > 65535) return NB_ERR_UNSUPPORTED;
-  // work items and the blocks of the row statistics fit 31 bits
+  // the row statistics take a block for 64 rows, and where all rows see few keys one more
+  // for 16: they fit 31 bits, and so do the work items
   const double rows = static_cast<double>(batch) * heads * (static_cast<double>(n) + 127);
-  if (rows > 3.0e10 || n > INT32_MAX - 512) return NB_ERR_UNSUPPORTED;
+  if (rows > 2.7e10 || n > INT32_MAX - 512) return NB_ERR_UNSUPPORTED;
   return NB_OK;
 }
 
