@@ -21,7 +21,9 @@
 // its visible pages (the pages of the sinks, then those of the window); warp w
 // takes every fourth page, brought by one bulk copy each into the warp's own
 // ring, and keeps its own maximum, sum and output.  The warps, and then the
-// shares, are joined by their maxima.  Bound by memory: the page bytes, once.
+// shares, are joined by their maxima.  It cannot do without the page bytes, once; what
+// sets its time is arithmetic, 690 instructions a page and warp (DRAM is at 24 to 32 %
+// of its rate), and 6 to 8 us that every block takes to start and to join.
 #include <math.h>
 
 #include <type_traits>
@@ -188,7 +190,10 @@ __device__ __forceinline__ void store_row(const Params& p, int d, int64_t row, i
 // d = 128 two blocks of 200 registers schedule better than three of 168: 57 us against
 // 62 at 32 ragged contexts of up to 8192 tokens, 45 either way at one of 2^20; four of
 // 128 take 79 and 58.  At d = 64 five blocks of 96 take 22.3 us where four take 18.5
-// (64 streams x 4100 visible tokens), and three 18.5.
+// (64 streams x 4100 visible tokens), and three 18.5.  Two sets of heads (16 share the
+// cache): at d = 64 three blocks take 57.4 us at 32 ragged contexts and 46.1 at one of
+// 2^20, two 62 and 60.4, four 63.5 and 49; at d = 128 one or two (the kernel wants 255
+// registers either way) 93.0 and 68.6, three 111 and 89.
 constexpr int blocks_per_sm(int d, int sets) { return d == 64 ? (sets == 1 ? 4 : 3) : 2; }
 
 // kSets: sets of eight heads (the columns of a product): 1 when at most eight
