@@ -372,68 +372,77 @@ __device__ int producer(const Params& p, const int* pre, uint32_t base, uint8_t*
   using C = Cfg<D, kDQ>;
   const uint32_t bar = base + C::oBar;
   const int count = item_count<kDQ>(p, pre);
-  int tc = 0, fixes = 0;
+  int fixes = 0;
   Ring<C::NX> ring;
-  int* taken = p.taken + (kDQ ? 1 : 0);
-  int fetched = lane == 0 ? atomicAdd(taken, 1) : 0;
-  for (int rd = 0;;) {
-    const int it = __shfl_sync(0xffffffffu, fetched, 0);
-    Item x;
-    if (it < count) {
-      if (lane == 0) fetched = atomicAdd(taken, 1);  // the next one, needed only after this
-      x = item<D, kDQ>(p, pre, it);
-      if (x.nch == 0) continue;
-    } else {
-      x.nch = -1;
-    }
-    const int q = rd % kItems;
-    if (!__all_sync(0xffffffffu,
-                    lane != 0 || mbar_wait(bar + 8 * (C::bIFree + q), ((rd / kItems) & 1) ^ 1)))
-      return kErrIFree;
-    if (lane == 0) {
-      *reinterpret_cast<Item*>(gbase + C::oItem + q * 64) = x;
-      mbar_arrive(bar + 8 * (C::bIFull + q));
-    }
-    ++rd;
-    if (x.nch < 0) break;
-    const int tb = tc % C::NT;
-    bool ok = true;
-    if (lane == 0) {
-      ok = mbar_wait(bar + 8 * (C::bTFree + tb), ((tc / C::NT) & 1) ^ 1);
-      if (ok) {
-        const uint32_t full = bar + 8 * (C::bTFull + tb);
-        mbar_arrive_expect_tx(full, 2 * C::kTile + (kDQ ? 2 * kRows * 4 : 0));
-        const uint32_t s = base + C::oTile + tb * 2 * C::kTile;
-        const int bh = x.b * (kDQ ? p.heads : p.kv_heads) + x.h;
-        if (kDQ) {  // the rows' statistics, padded to whole tiles
-          const int64_t at = static_cast<int64_t>(bh) * p.npad + x.tile * kRows;
-          const uint32_t sr = base + C::oRow + tb * 2 * kRows * 4;
-          bulk_load(sr, p.nlse2 + at, kRows * 4, full);
-          bulk_load(sr + kRows * 4, p.nd + at, kRows * 4, full);
-        }
+  Ring<C::NT> tile;
+  auto run = [&]() -> int {
+    int* taken = p.taken + (kDQ ? 1 : 0);
+    int fetched = lane == 0 ? atomicAdd(taken, 1) : 0;
+    for (int rd = 0;;) {
+      const int it = __shfl_sync(0xffffffffu, fetched, 0);
+      Item x;
+      if (it < count) {
+        if (lane == 0) fetched = atomicAdd(taken, 1);  // the next one, needed only after this
+        x = item<D, kDQ>(p, pre, it);
+        if (x.nch == 0) continue;
+      } else {
+        x.nch = -1;
+      }
+      const int q = rd % kItems;
+      if (!__all_sync(0xffffffffu,
+                      lane != 0 || mbar_wait(bar + 8 * (C::bIFree + q), ((rd / kItems) & 1) ^ 1)))
+        return kErrIFree;
+      if (lane == 0) {
+        *reinterpret_cast<Item*>(gbase + C::oItem + q * 64) = x;
+        mbar_arrive(bar + 8 * (C::bIFull + q));
+      }
+      ++rd;
+      if (x.nch < 0) break;
+      const int tb = tile.i;
+      bool ok = true;
+      if (lane == 0) {
+        ok = mbar_wait(bar + 8 * (C::bTFree + tb), tile.ph ^ 1);
+        if (ok) {
+          const uint32_t full = bar + 8 * (C::bTFull + tb);
+          mbar_arrive_expect_tx(full, 2 * C::kTile + (kDQ ? 2 * kRows * 4 : 0));
+          const uint32_t s = base + C::oTile + tb * 2 * C::kTile;
+          const int bh = x.b * (kDQ ? p.heads : p.kv_heads) + x.h;
+          if (kDQ) {  // the rows' statistics, padded to whole tiles
+            const int64_t at = static_cast<int64_t>(bh) * p.npad + x.tile * kRows;
+            const uint32_t sr = base + C::oRow + tb * 2 * kRows * 4;
+            bulk_load(sr, p.nlse2 + at, kRows * 4, full);
+            bulk_load(sr + kRows * 4, p.nd + at, kRows * 4, full);
+          }
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          tma_load_3d(s + i * kSlab, tx, full, i * 64, x.tile * kRows, bh);
-          tma_load_3d(s + C::kTile + i * kSlab, ty, full, i * 64, x.tile * kRows, bh);
+          for (int i = 0; i < D / 64; ++i) {
+            tma_load_3d(s + i * kSlab, tx, full, i * 64, x.tile * kRows, bh);
+            tma_load_3d(s + C::kTile + i * kSlab, ty, full, i * 64, x.tile * kRows, bh);
+          }
         }
       }
+      if (!__all_sync(0xffffffffu, ok)) return kErrTFree;
+      tile.next();
+      for (int c = 0; c < x.nch; ++c) {
+        if (!__all_sync(0xffffffffu,
+                        lane != 0 || mbar_wait(bar + 8 * (C::bXFree + ring.i), ring.ph ^ 1)))
+          return kErrXFree;
+        const int err = load_chunk<D, kDQ, !C::kSplit>(
+            p, x.L, chunk<D, kDQ>(p, x, c), base, gbase, kDQ && c < x.far ? cf : cx,
+            C::oX + ring.i * C::kHalf, cy, C::oY + ring.i * C::kHalf,
+            bar + 8 * (C::bXFull + ring.i), bar + 8 * C::bFix, fixes,
+            kDQ ? 0 : base + C::oCol + ring.i * 2 * C::kChunk * 4, lane);
+        if (err) return err;
+        ring.next();
+      }
     }
-    if (!__all_sync(0xffffffffu, ok)) return kErrTFree;
-    for (int c = 0; c < x.nch; ++c) {
-      if (!__all_sync(0xffffffffu,
-                      lane != 0 || mbar_wait(bar + 8 * (C::bXFree + ring.i), ring.ph ^ 1)))
-        return kErrXFree;
-      const int err = load_chunk<D, kDQ, !C::kSplit>(
-          p, x.L, chunk<D, kDQ>(p, x, c), base, gbase, kDQ && c < x.far ? cf : cx,
-          C::oX + ring.i * C::kHalf, cy, C::oY + ring.i * C::kHalf,
-          bar + 8 * (C::bXFull + ring.i), bar + 8 * C::bFix, fixes,
-          kDQ ? 0 : base + C::oCol + ring.i * 2 * C::kChunk * 4, lane);
-      if (err) return err;
-      ring.next();
-    }
-    ++tc;
-  }
-  return 0;
+    return 0;
+  };
+  const int err = run();
+  // copies that nobody took have landed before the block exits
+  if (err == kErrFix) mbar_wait(bar + 8 * C::bFix, fixes & 1);
+  drain_ring<C::NT>(tile.i, tile.ph, [&](int i, uint32_t ph) { mbar_wait(bar + 8 * (C::bTFull + i), ph); });
+  drain_ring<C::NX>(ring.i, ring.ph, [&](int i, uint32_t ph) { mbar_wait(bar + 8 * (C::bXFull + i), ph); });
+  return err;
 }
 
 // kSplit: the Y operand of the chunks (warp 3, the whole warp).
@@ -444,22 +453,28 @@ __device__ int y_producer(const Params& p, uint32_t base, uint8_t* gbase, int la
   const uint32_t bar = base + C::oBar;
   int fixes = 0;
   Ring<C::NY> ring;
-  for (int rd = 0;; ++rd) {
-    Item x;
-    if (!next_item<D, kDQ>(x, rd, bar, gbase, lane)) return kErrIFull;
-    if (x.nch < 0) break;
-    for (int c = 0; c < x.nch; ++c) {
-      if (!__all_sync(0xffffffffu,
-                      lane != 0 || mbar_wait(bar + 8 * (C::bYFree + ring.i), ring.ph ^ 1)))
-        return kErrYFree;
-      const int err = load_chunk<D, kDQ, false>(
-          p, x.L, chunk<D, kDQ>(p, x, c), base, gbase, cy, C::oY + ring.i * C::kHalf, nullptr, 0,
-          bar + 8 * (C::bYFull + ring.i), bar + 8 * (C::bFix + 1), fixes, 0, lane);
-      if (err) return err;
-      ring.next();
+  auto run = [&]() -> int {
+    for (int rd = 0;; ++rd) {
+      Item x;
+      if (!next_item<D, kDQ>(x, rd, bar, gbase, lane)) return kErrIFull;
+      if (x.nch < 0) break;
+      for (int c = 0; c < x.nch; ++c) {
+        if (!__all_sync(0xffffffffu,
+                        lane != 0 || mbar_wait(bar + 8 * (C::bYFree + ring.i), ring.ph ^ 1)))
+          return kErrYFree;
+        const int err = load_chunk<D, kDQ, false>(
+            p, x.L, chunk<D, kDQ>(p, x, c), base, gbase, cy, C::oY + ring.i * C::kHalf, nullptr, 0,
+            bar + 8 * (C::bYFull + ring.i), bar + 8 * (C::bFix + 1), fixes, 0, lane);
+        if (err) return err;
+        ring.next();
+      }
     }
-  }
-  return 0;
+    return 0;
+  };
+  const int err = run();
+  if (err == kErrFix) mbar_wait(bar + 8 * (C::bFix + 1), fixes & 1);
+  drain_ring<C::NY>(ring.i, ring.ph, [&](int i, uint32_t ph) { mbar_wait(bar + 8 * (C::bYFull + i), ph); });
+  return err;
 }
 
 // Number of chunks of the rd-th item, for the single-thread roles (the rest of the
@@ -1102,6 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     regs_dec<C::kRegsEpi, kLaunchRegs>();
     err = epi_warps<D, kDQ>(p, base, gbase, tmem, warp & 3, lane, &to0, &to1);
+    if (err) bulk_wait_all0();  // a store that is still reading the staging
   }
   if (err) record_error(p.err, err);
 

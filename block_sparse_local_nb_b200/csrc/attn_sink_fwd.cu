@@ -226,38 +226,45 @@ __device__ int producer(const Params& p, const Sched& sch, uint32_t base, uint8_
   const uint32_t bar = base + C::oBar;
   Ring<C::NQ> qr;
   Ring<C::NKV> kr;
-  for (int rd = 0;; ++rd) {
-    const int it = item_at(rd), i = rd % kItems;
-    Item x;
-    if (it < sch.count) x = sched_item(p, sch, it);
-    else x.nch = -1;
-    if (!mbar_wait(bar + 8 * (C::bIFree + i), ((rd / kItems) & 1) ^ 1)) return kErrIFree;
-    *reinterpret_cast<Item*>(gbase + C::oItem + i * 32) = x;
-    mbar_arrive(bar + 8 * (C::bIFull + i));
-    if (x.nch < 0) break;
-    if (x.nch == 0) continue;
-    const int bh = x.b * p.a.heads + x.h, bkv = bh / p.group;
-    if (!mbar_wait(bar + 8 * (C::bQFree + qr.i), qr.ph ^ 1)) return kErrQFree;
-    mbar_arrive_expect_tx(bar + 8 * (C::bQFull + qr.i), C::kQBytes);
+  auto run = [&]() -> int {
+    for (int rd = 0;; ++rd) {
+      const int it = item_at(rd), i = rd % kItems;
+      Item x;
+      if (it < sch.count) x = sched_item(p, sch, it);
+      else x.nch = -1;
+      if (!mbar_wait(bar + 8 * (C::bIFree + i), ((rd / kItems) & 1) ^ 1)) return kErrIFree;
+      *reinterpret_cast<Item*>(gbase + C::oItem + i * 32) = x;
+      mbar_arrive(bar + 8 * (C::bIFull + i));
+      if (x.nch < 0) break;
+      if (x.nch == 0) continue;
+      const int bh = x.b * p.a.heads + x.h, bkv = bh / p.group;
+      if (!mbar_wait(bar + 8 * (C::bQFree + qr.i), qr.ph ^ 1)) return kErrQFree;
+      mbar_arrive_expect_tx(bar + 8 * (C::bQFull + qr.i), C::kQBytes);
 #pragma unroll
-    for (int s = 0; s < D / 64; ++s)
-      tma_load_3d(base + C::oQ + qr.i * C::kQBytes + s * kSlab, tq, bar + 8 * (C::bQFull + qr.i),
-                  s * 64, x.tile * kRows, bh);
-    qr.next();
-    for (int c = 0; c < x.nch; ++c) {
-      if (!mbar_wait(bar + 8 * (C::bSFull + kr.i), kr.ph ^ 1)) return kErrKFree;
-      const uint32_t full = bar + 8 * (C::bKFull + kr.i);
-      mbar_arrive_expect_tx(full, C::kKBytes);
+      for (int s = 0; s < D / 64; ++s)
+        tma_load_3d(base + C::oQ + qr.i * C::kQBytes + s * kSlab, tq, bar + 8 * (C::bQFull + qr.i),
+                    s * 64, x.tile * kRows, bh);
+      qr.next();
+      for (int c = 0; c < x.nch; ++c) {
+        if (!mbar_wait(bar + 8 * (C::bSFull + kr.i), kr.ph ^ 1)) return kErrKFree;
+        const uint32_t full = bar + 8 * (C::bKFull + kr.i);
+        mbar_arrive_expect_tx(full, C::kKBytes);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int s = 0; s < D / 64; ++s)
-          tma_load_3d(base + C::oK + kr.i * C::kKBytes + s * kSlab + h * kHalf * 128, tk, full,
-                      s * 64, x.key(2 * c + h), bkv);
-      kr.next();
+          for (int s = 0; s < D / 64; ++s)
+            tma_load_3d(base + C::oK + kr.i * C::kKBytes + s * kSlab + h * kHalf * 128, tk, full,
+                        s * 64, x.key(2 * c + h), bkv);
+        kr.next();
+      }
     }
-  }
-  return 0;
+    return 0;
+  };
+  const int err = run();
+  // copies that nobody took have landed before the block exits
+  drain_ring<C::NQ>(qr.i, qr.ph, [&](int i, uint32_t ph) { mbar_wait(bar + 8 * (C::bQFull + i), ph); });
+  drain_ring<C::NKV>(kr.i, kr.ph, [&](int i, uint32_t ph) { mbar_wait(bar + 8 * (C::bKFull + i), ph); });
+  return err;
 }
 
 // V chunks (warp 3, the whole warp; lane 0 issues).  A chunk that reaches past
@@ -270,48 +277,54 @@ __device__ int v_producer(const Params& p, uint32_t base, uint8_t* gbase, int la
   const uint32_t bar = base + C::oBar;
   int fixes = 0;
   Ring<C::NKV> vr;
-  for (int rd = 0;; ++rd) {
-    Item x;
-    if (!next_item<D>(x, rd, bar, gbase, lane)) return kErrIFull;
-    if (x.nch < 0) break;
-    const int bkv = (x.b * p.a.heads + x.h) / p.group;
-    for (int c = 0; c < x.nch; ++c) {
-      const int st = vr.i;
-      const int y[2] = {x.key(2 * c), x.key(2 * c + 1)};
-      // rows of a block from L - y on hold other data
-      const bool fix = max(y[0], y[1]) + kHalf > x.L && x.L < p.a.n;
-      const uint32_t full = bar + 8 * (C::bVFull + st);
-      const uint32_t land = fix ? bar + 8 * C::bVFix : full;
-      bool ok = true;
-      if (lane == 0) {
-        ok = mbar_wait(bar + 8 * (C::bSFree + st), vr.ph ^ 1);
-        if (ok) {
-          mbar_arrive_expect_tx(land, C::kKBytes);
+  auto run = [&]() -> int {
+    for (int rd = 0;; ++rd) {
+      Item x;
+      if (!next_item<D>(x, rd, bar, gbase, lane)) return kErrIFull;
+      if (x.nch < 0) break;
+      const int bkv = (x.b * p.a.heads + x.h) / p.group;
+      for (int c = 0; c < x.nch; ++c) {
+        const int st = vr.i;
+        const int y[2] = {x.key(2 * c), x.key(2 * c + 1)};
+        // rows of a block from L - y on hold other data
+        const bool fix = max(y[0], y[1]) + kHalf > x.L && x.L < p.a.n;
+        const uint32_t full = bar + 8 * (C::bVFull + st);
+        const uint32_t land = fix ? bar + 8 * C::bVFix : full;
+        bool ok = true;
+        if (lane == 0) {
+          ok = mbar_wait(bar + 8 * (C::bSFree + st), vr.ph ^ 1);
+          if (ok) {
+            mbar_arrive_expect_tx(land, C::kKBytes);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int s = 0; s < D / 64; ++s)
-              tma_load_3d(base + C::oV + st * C::kKBytes + s * kSlab + h * kHalf * 128,
-                          2 * c + h < x.far ? tf : tv, land, s * 64, y[h], bkv);
+              for (int s = 0; s < D / 64; ++s)
+                tma_load_3d(base + C::oV + st * C::kKBytes + s * kSlab + h * kHalf * 128,
+                            2 * c + h < x.far ? tf : tv, land, s * 64, y[h], bkv);
+          }
         }
+        if (!__all_sync(0xffffffffu, ok)) return kErrVFree;
+        if (fix) {
+          if (!__all_sync(0xffffffffu, mbar_wait(land, fixes & 1))) return kErrVFix;
+          ++fixes;
+          uint4* v = reinterpret_cast<uint4*>(gbase + C::oV + st * C::kKBytes);
+          for (int h = 0; h < 2; ++h)  // whole 128-byte rows, so the swizzle does not matter
+            for (int s = 0; s < D / 64; ++s)
+              for (int i = max(x.L - y[h], 0) * 8 + lane; i < kHalf * 8; i += 32)
+                v[s * (kSlab / 16) + h * kHalf * 8 + i] = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full);
+        }
+        vr.next();
       }
-      if (!__all_sync(0xffffffffu, ok)) return kErrVFree;
-      if (fix) {
-        if (!__all_sync(0xffffffffu, mbar_wait(land, fixes & 1))) return kErrVFix;
-        ++fixes;
-        uint4* v = reinterpret_cast<uint4*>(gbase + C::oV + st * C::kKBytes);
-        for (int h = 0; h < 2; ++h)  // whole 128-byte rows, so the swizzle does not matter
-          for (int s = 0; s < D / 64; ++s)
-            for (int i = max(x.L - y[h], 0) * 8 + lane; i < kHalf * 8; i += 32)
-              v[s * (kSlab / 16) + h * kHalf * 8 + i] = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full);
-      }
-      vr.next();
     }
-  }
-  return 0;
+    return 0;
+  };
+  const int err = run();
+  if (err == kErrVFix) mbar_wait(bar + 8 * C::bVFix, fixes & 1);
+  drain_ring<C::NKV>(vr.i, vr.ph, [&](int i, uint32_t ph) { mbar_wait(bar + 8 * (C::bVFull + i), ph); });
+  return err;
 }
 
 // S = Q K^T for every chunk into S buffer G % NSB (warp 1, one thread).  P of
@@ -787,6 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     regs_dec<C::kRegsEpi, kLaunchRegs>();
     err = epi_warps<D>(p, base, gbase, tmem, warp & 3, lane, &to);
+    if (err) bulk_wait_all0();  // a store that is still reading the staging
     named_barrier(3, 384);
   }
   if (err) record_error(p.a.err, err);

@@ -109,6 +109,15 @@ struct Ring {
   }
 };
 
+// A ring of N stages, each with a barrier that completes a phase when its copy has landed,
+// and nothing else: i and ph are where the next copy would go and its phase's parity.  Calls
+// wait(stage, parity) for the last copy of each; it returns at once where none is in flight.
+template <int N, class Wait>
+__host__ __device__ __forceinline__ void drain_ring(int i, uint32_t ph, Wait&& wait) {
+#pragma unroll 1
+  for (int s = 0; s < N; ++s) wait(s, s < i ? ph : ph ^ 1u);
+}
+
 // d = a b + c (a row-major 16 x 16, b 16 x 8, bf16 in, fp32 out).
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1, const float (&c)[4]) {
