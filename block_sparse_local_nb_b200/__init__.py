@@ -9,6 +9,10 @@ and raises if the library was not built.
 from .binding import (  # noqa: F401
     NB_BF16,
     NB_F32,
+    NB_KERR_KV4_DECODE,
+    NB_KERR_KV4_READ,
+    NB_KERR_KV4_WRITE,
+    NB_KERR_WAIT,
     NbError,
     attn_bwd_workspace_size,
     attn_fwd_bwd_host_workspace_size,

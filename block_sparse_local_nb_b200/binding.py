@@ -16,6 +16,10 @@ import threading
 
 NB_F32 = 0
 NB_BF16 = 1
+NB_KERR_WAIT = 0x100       # nb_kernel_error: a wait ran out, outputs are undefined
+NB_KERR_KV4_WRITE = 0x51   # nb_kv4_write skipped a token
+NB_KERR_KV4_READ = 0x52    # nb_kv4_read wrote 0 for a token
+NB_KERR_KV4_DECODE = 0x53  # nb_attn_kv4_decode did not see a page
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnb_b200.so")
 _lock = threading.Lock()

@@ -56,3 +56,9 @@ int main() {
     wait = codes["NB_KERR_WAIT"] | 0x51
     # a reset of the word that was reported leaves the other for the next call
     assert got == [(0, 1), (codes["NB_KERR_KV4_WRITE"], 1), (wait, 0), (wait, 0)]
+
+
+def test_the_binding_has_the_public_codes():
+    import block_sparse_local_nb_b200 as nb
+
+    assert public_codes() and all(getattr(nb, n) == v for n, v in public_codes().items())
